@@ -314,6 +314,159 @@ LH_API lh_status lh_search_amax(const void* W, lh_dtype w_dtype, int64_t n_mats,
                          int64_t ld_w, const float* global_amax, const float* H, double start, double step,
                          int64_t n_mult, float* best_amax, uint8_t* best_code, void* stream);
 
+/* ========================================================================
+ * Running a calibrated layer: NVFP4 tokens, products, and tokens sorted by
+ * expert. The pages describe calibration and W4A4 accuracy ("NVIDIA Model
+ * Optimizer Local-Hessian ..." section "仅更好的缩放，零运行时成本": the better
+ * scales cost nothing at run time); they give no formulas for the run time, so
+ * the definitions below are this library's own.
+ * ===================================================================== */
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert: the token groups that lh_accumulate_hessian and the
+ * products below take, from a router's choices. With the flat index f = t*k + s
+ * of slot s of token t:
+ *   order = the f with 0 <= ids[f] < n_experts, sorted by (ids[f], f);
+ *   pos[order[p]] = p;
+ *   offsets[e] = how many of them have an expert below e.
+ * Any other id (-1, say, for a masked token) belongs to no expert: pos[f] = -1,
+ * and order holds -1 from offsets[n_experts] on. The sort is stable and uses no
+ * atomics: the same ids give the same order. An expert may occur twice in a token.
+ * ids: device int32 [n_tok][k]. offsets: device int64 [n_experts + 1]. order, pos:
+ *   device int32 [n_tok * k]. All of them are written in full.
+ * One launch; n_tok == 0 only writes zero offsets.
+ * LH_ERR_UNSUPPORTED: n_experts > 1024, or n_tok * k >= 2^31.
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_route_tokens(const int32_t* ids, int64_t n_tok, int64_t k, int64_t n_experts, int64_t* offsets,
+                                 int32_t* order, int32_t* pos, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rows in sorted order: Xs[p] = X[order[p] / k] for p < n_rows. Rows whose order
+ * is negative, or names a token past n_tok, are left as they were, and so are the
+ * columns from c to ld_xs. The gradient with respect to X is lh_combine_tokens with
+ * weights = NULL on the gradient of Xs.
+ * X: device bf16 or f32 [n_tok][ld_x]. Xs: device, the same type, [n_rows][ld_xs].
+ * order: device int32 [n_rows] (lh_route_tokens; k = 1 copies plain rows).
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_tok, int64_t c, int64_t ld_x,
+                                  const int32_t* order, int64_t k, int64_t n_rows, void* Xs, int64_t ld_xs,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' rows back to the tokens:
+ *   Y[t] = cast( sum_s weights[t][s] * Ys[pos[t*k + s]] ),
+ * summed in FP32 over s in order; slots whose pos is negative or >= n_rows add
+ * nothing, and a token without any gets zeros. Rows of Ys that no pos names are not
+ * read. weights: device f32 [n_tok][k], or NULL for ones.
+ * Ys: device bf16 or f32 [n_rows][ld_ys]. Y: device, the same type, [n_tok][ld_y];
+ *   its columns from c to ld_y are left as they were. pos: device int32 [n_tok * k].
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n_rows, int64_t c, int64_t ld_ys,
+                                   const int32_t* pos, const float* weights, int64_t n_tok, int64_t k, void* Y,
+                                   int64_t ld_y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient of lh_combine_tokens for dY, the gradient of Y:
+ *   dYs[pos[f]] = cast( weights[f] * dY[t] ),   dweights[f] = <dY[t], Ys[pos[f]]>
+ * for f = t*k + s; the products and sums are FP32, in a fixed order (no atomics).
+ * Slots without a row get dweights 0; rows of dYs that no pos names are left as they
+ * were. Each row of dYs must be named once (as lh_route_tokens's pos does); a row
+ * named twice keeps one of the two. dYs or dweights may be NULL (not wanted; Ys is
+ * then needed for dweights only). weights may be NULL (ones).
+ * dY: device bf16 or f32 [n_tok][ld_dy]; Ys, dYs: the same type, [n_rows][ld_ys],
+ * [n_rows][ld_dys]. dweights: device f32 [n_tok][k].
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int64_t n_tok, int64_t k, int64_t c,
+                                        int64_t ld_dy, const void* Ys, int64_t ld_ys, int64_t n_rows,
+                                        const int32_t* pos, const float* weights, void* dYs, int64_t ld_dys,
+                                        float* dweights, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Scale tiles: the order in which the products read E4M3 block scales. 128 rows x 4
+ * blocks make a tile of 512 bytes, byte (r, j) at 16 (r % 32) + 4 (r / 32) + j; the
+ * ceil(c_in / 64) tiles of the same 128 rows follow one another, then those of the
+ * next 128 rows. Weights: each matrix starts on a tile of its own. Tokens: group g
+ * starts on tile row offsets[g] / 128 + g. Blocks past c_in are 0; rows past a
+ * matrix are 0, rows past a group are unspecified and never used.
+ * lh_nvfp4_tile_scales brings the bytes of lh_quantize_nvfp4 (block_scales, device u8
+ * [n_mats][c_out][c_in/16]) into that order, once per exported layer; tiles: device,
+ * 16-byte aligned, lh_nvfp4_weight_scale_bytes(n_mats, c_out, c_in) bytes.
+ * Both sizes are 0 for invalid arguments.
+ * ---------------------------------------------------------------------- */
+LH_API size_t lh_nvfp4_weight_scale_bytes(int64_t n_mats, int64_t c_out, int64_t c_in);
+LH_API size_t lh_nvfp4_token_scale_bytes(int64_t n_rows, int64_t c_in, int64_t n_groups);
+LH_API lh_status lh_nvfp4_tile_scales(const uint8_t* block_scales, int64_t n_mats, int64_t c_out, int64_t c_in,
+                                      uint8_t* tiles, void* stream);
+
+/* ------------------------------------------------------------------------
+ * NVFP4 quantisation of tokens with max scaling (LH_SCALE_MAX's formula), with the
+ * global scale from the token itself or from a given amax:
+ *   x   = X[rows[p] / row_div] for row p < n_rows (rows NULL: X[p], row_div 1)
+ *   g   = fp32(amax / 2688), amax = max |x| of the token, or global_amax[0]
+ *   v_b = E4M3_RNE_sat(fp32(fp32(amax_b / 6) / g)), at least code 1 (code 1 if g == 0)
+ *   q   = E2M1_RNE_sat(fp32(x / s)), s = fp32(v_b * g)   (+-0 if s == 0)
+ * token_scale[p] = g; packed[p][c/2] holds the codes of q as in lh_quantize_nvfp4;
+ * scale_tiles holds v_b's codes (see above). X_out (optional) gets fp32(q * s) cast to
+ * out_dtype, the fake-quantised tokens.
+ * A token that holds an infinity or a NaN gets token_scale NaN, so its products are
+ * NaN. Blocks with such a value (every block of the token when the scale is the
+ * token's own) get code 0x7F (NaN) and NaN in X_out. A given global_amax must be
+ * finite and >= 0 and is not checked; larger values saturate.
+ * offsets: device int64 [n_groups + 1], non-decreasing: the rows of each group (NULL:
+ *   one group, n_groups 1); they place the scale tiles. Values are clamped to
+ *   [0, n_rows]. Decreasing offsets are not detected: accesses stay in bounds, results
+ *   are unspecified. Outputs of rows that lie in no group, and of rows whose source is
+ *   negative or past n_src, are left as they were.
+ * X: device bf16 or f32 [n_src][ld_x]. rows: device int32 [n_rows] or NULL.
+ * global_amax: device f32 [1] or NULL. packed: device u8 [n_rows][c_in/2], 16-byte
+ *   aligned. scale_tiles: device, 16-byte aligned, lh_nvfp4_token_scale_bytes(n_rows,
+ *   c_in, n_groups) bytes. token_scale: device f32 [n_rows]. X_out: device
+ *   [n_rows][c_in], bf16 or f32.
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c_in, int64_t ld_x,
+                                    const int32_t* rows, int64_t row_div, int64_t n_rows, const int64_t* offsets,
+                                    int64_t n_groups, const float* global_amax, uint8_t* packed,
+                                    uint8_t* scale_tiles, float* token_scale, void* X_out, lh_dtype out_dtype,
+                                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * Product of NVFP4 tokens and NVFP4 weights (W4A4), one matrix per group of tokens:
+ *   Y[t][r] = cast( X_gscale[t] * W_gscale[m] *
+ *                   sum_j vx[t][j] * vw[m][r][j] * sum_i qx[t][16j+i] * qw[m][r][16j+i] )
+ * for the tokens t of group m (offsets as in lh_quantize_tokens; NULL: one matrix and
+ * all tokens). Sums are FP32 on the tensor cores, in an order fixed by the sizes.
+ * X_packed, X_scales, X_gscale: as lh_quantize_tokens writes them (n_rows tokens, the
+ *   same offsets). W_packed: device u8 [n_groups][c_out][c_in/2] and W_gscale: device
+ *   f32 [n_groups], as lh_quantize_nvfp4 writes them; W_scales: lh_nvfp4_tile_scales.
+ * Y: device bf16 (round to nearest even) or f32 [n_rows][ld_y]; rows in no group and
+ *   columns from c_out to ld_y are left as they were.
+ * c_in: a positive multiple of 32. n_rows, c_in and n_groups * c_out below 2^31 - 512.
+ * Waits inside the kernel are bounded (1 s). One that gives up leaves Y incomplete and
+ * is reported by lh_nvfp4_status, which synchronises `stream`, returns LH_ERR_TIMEOUT
+ * if that happened on the current device since the last call, and clears it.
+ * ---------------------------------------------------------------------- */
+LH_API lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale,
+                                 const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale,
+                                 const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out,
+                                 int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, void* stream);
+LH_API lh_status lh_nvfp4_status(void* stream);
+
+/* ------------------------------------------------------------------------
+ * lh_quantize_tokens and lh_nvfp4_matmul in one call: Y = Xq Wq^T from the tokens
+ * themselves, with the arguments of the two. The quantised tokens live in `workspace`
+ * (device, 256-byte aligned, lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups)
+ * bytes, no clearing needed; not to be shared by calls in flight at the same time, nor
+ * by two captured graphs that may run at the same time).
+ * Rows whose source is negative or past n_src have unspecified results.
+ * ---------------------------------------------------------------------- */
+LH_API size_t lh_nvfp4_linear_workspace_bytes(int64_t n_rows, int64_t c_in, int64_t n_groups);
+LH_API lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c_in, int64_t ld_x,
+                                 const int32_t* rows, int64_t row_div, int64_t n_rows, const int64_t* offsets,
+                                 int64_t n_groups, const float* global_amax, const uint8_t* W_packed,
+                                 const uint8_t* W_scales, const float* W_gscale, int64_t c_out, void* Y,
+                                 lh_dtype out_dtype, int64_t ld_y, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 #ifdef __cplusplus
 }
 #endif

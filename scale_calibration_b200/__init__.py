@@ -18,6 +18,9 @@ from ._binding import (  # noqa: F401
     lh_quantize_nvfp4, lh_sweep_scales, lh_workspace_status, lh_baseline_scales, LH_SCALE_MAX,
     LH_SCALE_FOUR_OVER_SIX, LH_SCALE_MSE, lh_search_amax, lh_sweep_scales_ws, lh_sweep_workspace_bytes,
     lh_probe_fma, lh_probe_fma_flop,
+    lh_route_tokens, lh_gather_tokens, lh_combine_tokens, lh_combine_tokens_grad, lh_quantize_tokens,
+    lh_nvfp4_weight_scale_bytes, lh_nvfp4_token_scale_bytes, lh_nvfp4_tile_scales, lh_nvfp4_matmul, lh_nvfp4_status,
+    lh_nvfp4_linear_workspace_bytes, lh_nvfp4_linear,
 )
 
 

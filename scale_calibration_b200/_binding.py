@@ -21,6 +21,9 @@ EXPORTS = [
     "lh_accumulate_hessian", "lh_workspace_status", "lh_sweep_scales", "lh_fake_quant",
     "lh_accumulate_hessian_noalloc", "lh_noalloc_status", "lh_debug_wait_timeout", "lh_quantize_nvfp4", "lh_baseline_scales",
     "lh_search_amax", "lh_sweep_workspace_bytes", "lh_sweep_scales_ws", "lh_probe_fma", "lh_probe_fma_flop", "lh_debug_sweep_counts",
+    "lh_route_tokens", "lh_gather_tokens", "lh_combine_tokens", "lh_combine_tokens_grad",
+    "lh_nvfp4_weight_scale_bytes", "lh_nvfp4_token_scale_bytes", "lh_nvfp4_tile_scales", "lh_quantize_tokens",
+    "lh_nvfp4_matmul", "lh_nvfp4_status", "lh_nvfp4_linear_workspace_bytes", "lh_nvfp4_linear",
 ]
 LH_SCALE_MAX, LH_SCALE_FOUR_OVER_SIX, LH_SCALE_MSE = range(3)
 
@@ -56,6 +59,19 @@ def _load() -> ctypes.CDLL:
         "lh_probe_fma_flop": (I64, [I64, I64]),
         "lh_probe_fma": (I32, [I32, I64, I64, P, P]),
         "lh_debug_sweep_counts": (I32, [P, I32]),
+        "lh_route_tokens": (I32, [P, I64, I64, I64, P, P, P, P]),
+        "lh_gather_tokens": (I32, [P, I32, I64, I64, I64, P, I64, I64, P, I64, P]),
+        "lh_combine_tokens": (I32, [P, I32, I64, I64, I64, P, P, I64, I64, P, I64, P]),
+        "lh_combine_tokens_grad": (I32, [P, I32, I64, I64, I64, I64, P, I64, I64, P, P, P, I64, P, P]),
+        "lh_nvfp4_weight_scale_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+        "lh_nvfp4_token_scale_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+        "lh_nvfp4_tile_scales": (I32, [P, I64, I64, I64, P, P]),
+        "lh_quantize_tokens": (I32, [P, I32, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, P, I32, P]),
+        "lh_nvfp4_matmul": (I32, [P, P, P, P, P, P, P, I64, I64, I64, I64, P, I32, I64, P]),
+        "lh_nvfp4_status": (I32, [P]),
+        "lh_nvfp4_linear_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+        "lh_nvfp4_linear": (I32, [P, I32, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, I64, P, I32, I64, P,
+                                  ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -226,4 +242,90 @@ def lh_search_amax(W, w_dtype, n_mats, c_out, c_in, ld_w, global_amax, H, best_a
                             float(start), float(step), int(n_mult), _ptr(best_amax), _ptr(best_code), _stream(stream))
     if check:
         _check(s, "lh_search_amax")
+    return s
+
+
+def lh_route_tokens(ids, n_tok, k, n_experts, offsets, order, pos, stream=None, check=True) -> int:
+    s = _lib.lh_route_tokens(_ptr(ids), n_tok, k, n_experts, _ptr(offsets), _ptr(order), _ptr(pos), _stream(stream))
+    if check:
+        _check(s, "lh_route_tokens")
+    return s
+
+
+def lh_gather_tokens(X, dtype, n_tok, c, ld_x, order, k, n_rows, Xs, ld_xs, stream=None, check=True) -> int:
+    s = _lib.lh_gather_tokens(_ptr(X), _dtype(dtype), n_tok, c, ld_x, _ptr(order), k, n_rows, _ptr(Xs), ld_xs,
+                              _stream(stream))
+    if check:
+        _check(s, "lh_gather_tokens")
+    return s
+
+
+def lh_combine_tokens(Ys, dtype, n_rows, c, ld_ys, pos, weights, n_tok, k, Y, ld_y, stream=None, check=True) -> int:
+    s = _lib.lh_combine_tokens(_ptr(Ys), _dtype(dtype), n_rows, c, ld_ys, _ptr(pos), _ptr(weights), n_tok, k, _ptr(Y),
+                               ld_y, _stream(stream))
+    if check:
+        _check(s, "lh_combine_tokens")
+    return s
+
+
+def lh_combine_tokens_grad(dY, dtype, n_tok, k, c, ld_dy, Ys, ld_ys, n_rows, pos, weights, dYs, ld_dys, dweights,
+                           stream=None, check=True) -> int:
+    s = _lib.lh_combine_tokens_grad(_ptr(dY), _dtype(dtype), n_tok, k, c, ld_dy, _ptr(Ys), ld_ys, n_rows, _ptr(pos),
+                                    _ptr(weights), _ptr(dYs), ld_dys, _ptr(dweights), _stream(stream))
+    if check:
+        _check(s, "lh_combine_tokens_grad")
+    return s
+
+
+def lh_nvfp4_weight_scale_bytes(n_mats, c_out, c_in) -> int:
+    return int(_lib.lh_nvfp4_weight_scale_bytes(n_mats, c_out, c_in))
+
+
+def lh_nvfp4_token_scale_bytes(n_rows, c_in, n_groups) -> int:
+    return int(_lib.lh_nvfp4_token_scale_bytes(n_rows, c_in, n_groups))
+
+
+def lh_nvfp4_tile_scales(block_scales, n_mats, c_out, c_in, tiles, stream=None, check=True) -> int:
+    s = _lib.lh_nvfp4_tile_scales(_ptr(block_scales), n_mats, c_out, c_in, _ptr(tiles), _stream(stream))
+    if check:
+        _check(s, "lh_nvfp4_tile_scales")
+    return s
+
+
+def lh_quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
+                       scale_tiles, token_scale, X_out=None, out_dtype=LH_BF16, stream=None, check=True) -> int:
+    s = _lib.lh_quantize_tokens(_ptr(X), _dtype(x_dtype), n_src, c_in, ld_x, _ptr(rows), row_div, n_rows,
+                                _ptr(offsets), n_groups, _ptr(global_amax), _ptr(packed), _ptr(scale_tiles),
+                                _ptr(token_scale), _ptr(X_out), _dtype(out_dtype), _stream(stream))
+    if check:
+        _check(s, "lh_quantize_tokens")
+    return s
+
+
+def lh_nvfp4_matmul(X_packed, X_scales, X_gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in,
+                    Y, out_dtype, ld_y, stream=None, check=True) -> int:
+    s = _lib.lh_nvfp4_matmul(_ptr(X_packed), _ptr(X_scales), _ptr(X_gscale), _ptr(W_packed), _ptr(W_scales),
+                             _ptr(W_gscale), _ptr(offsets), n_groups, n_rows, c_out, c_in, _ptr(Y), _dtype(out_dtype),
+                             ld_y, _stream(stream))
+    if check:
+        _check(s, "lh_nvfp4_matmul")
+    return s
+
+
+def lh_nvfp4_status(stream=None) -> int:
+    return _lib.lh_nvfp4_status(_stream(stream))
+
+
+def lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups) -> int:
+    return int(_lib.lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups))
+
+
+def lh_nvfp4_linear(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, W_packed,
+                    W_scales, W_gscale, c_out, Y, out_dtype, ld_y, workspace, workspace_bytes, stream=None,
+                    check=True) -> int:
+    s = _lib.lh_nvfp4_linear(_ptr(X), _dtype(x_dtype), n_src, c_in, ld_x, _ptr(rows), row_div, n_rows, _ptr(offsets),
+                             n_groups, _ptr(global_amax), _ptr(W_packed), _ptr(W_scales), _ptr(W_gscale), c_out,
+                             _ptr(Y), _dtype(out_dtype), ld_y, _ptr(workspace), workspace_bytes, _stream(stream))
+    if check:
+        _check(s, "lh_nvfp4_linear")
     return s

@@ -1,0 +1,462 @@
+// Tokens sorted by expert, and back.
+//
+// A bank of experts (one matrix per expert, as the Hessian, the sweep and the
+// products take it) wants the rows of one expert next to one another, with
+// offsets. These entry points make that order from the router's expert ids,
+// copy rows into it, and bring the experts' results back to the tokens with the
+// router's weights, with the gradient of that step.
+//
+//   flat index f = t * k + s (token t, slot s), expert ids[f];
+//   order = the valid f sorted by (ids[f], f);  pos[order[p]] = p;
+//   gather:   Xs[p] = X[order[p] / k]
+//   combine:  Y[t]  = sum_s w[t][s] * Ys[pos[t][s]]
+//   gradient: dYs[pos[t][s]] = w[t][s] * dY[t],  dw[t][s] = <dY[t], Ys[pos[t][s]]>
+#include <climits>
+
+#include "common.cuh"
+
+namespace lh {
+namespace {
+
+// ---------------------------------------------------------------- route
+
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kMaxExperts = 1024;  // one thread per expert in the scan
+constexpr int kRouteCluster = 8;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// A stable counting sort in one launch: one cluster, each CTA a contiguous chunk of
+// the ids, each warp a contiguous run of its chunk. Every warp counts its run into a
+// histogram of its own (lanes with the same expert find one another with match.any,
+// the first of them adds), the counts become prefixes over warps, CTAs (through
+// distributed shared memory) and experts, and every warp walks its run again and
+// hands out places in order. No atomics: the order is that of the flat index.
+__global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __restrict__ ids, int n, int E,
+                                                                 int64_t* __restrict__ offsets,
+                                                                 int* __restrict__ order, int* __restrict__ pos) {
+    extern __shared__ uint32_t sm[];
+    uint32_t* total = sm;          // [E] this CTA's count per expert
+    uint32_t* base = total + E;    // [E] first place of this CTA's rows of an expert
+    uint32_t* hist = base + E;     // [warps][E]
+    __shared__ uint32_t wsum[kRouteWarps];
+    __shared__ uint32_t n_valid;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    for (int i = tid; i < kRouteWarps * E; i += kRouteThreads) hist[i] = 0u;
+    __syncthreads();
+
+    const int64_t per_warp = (((int64_t)n + ranks * kRouteThreads - 1) / (ranks * kRouteThreads)) * 32;
+    const int64_t w0 = ((int64_t)rank * kRouteWarps + warp) * per_warp;
+    const int f0 = (int)(w0 < n ? w0 : n);
+    const int f1 = (int)(w0 + per_warp < n ? w0 + per_warp : n);
+    uint32_t* mine = hist + warp * E;
+    auto expert_of = [&](int f) {
+        const int e = f < f1 ? __ldg(ids + f) : -1;
+        return e >= 0 && e < E ? e : -1;
+    };
+    for (int f = f0 + lane; f - lane < f1; f += 32) {
+        const int e = expert_of(f);
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (tid < E) {  // counts -> prefixes over the CTA's warps
+        uint32_t sum = 0;
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const uint32_t c = hist[w * E + tid];
+            hist[w * E + tid] = sum;
+            sum += c;
+        }
+        total[tid] = sum;
+    }
+    cluster_sync();
+    uint32_t all = 0, before = 0;
+    if (tid < E) {
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const uint32_t c = ld_remote(total + tid, r);
+            if (r < rank) before += c;
+            all += c;
+        }
+    }
+    // inclusive scan of `all` over the experts
+    uint32_t inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t s = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += v;
+        }
+        wsum[lane] = s;
+    }
+    __syncthreads();
+    inc += warp ? wsum[warp - 1] : 0u;
+    if (tid < E) {
+        base[tid] = inc - all + before;
+        if (rank == 0) {
+            offsets[tid + 1] = (int64_t)inc;
+            if (tid == 0) offsets[0] = 0;
+        }
+        if (tid == E - 1) n_valid = inc;
+    }
+    __syncthreads();
+    for (int f = f0 + lane; f - lane < f1; f += 32) {
+        const int e = expert_of(f);
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        int p = -1;
+        if (e >= 0) p = (int)(base[e] + mine[e] + __popc(same & ((1u << lane) - 1u)));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (f < f1) pos[f] = p;
+        if (p >= 0) order[p] = f;
+    }
+    for (int64_t p = (int64_t)n_valid + rank * kRouteThreads + tid; p < n; p += ranks * kRouteThreads) order[p] = -1;
+    cluster_sync();  // a CTA's counts stay readable until every CTA has read them
+}
+
+// ---------------------------------------------------------------- rows
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+
+template <typename T>
+struct Row16;  // 16 bytes of a row as floats
+template <>
+struct Row16<uint16_t> {
+    static constexpr int kN = 8;
+    __device__ static void unpack(const uint4& v, float (&x)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ static uint4 pack(const float (&x)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ static float one(uint16_t v) { return bf16_bits_to_float(v); }
+    __device__ static uint16_t rounded(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+template <>
+struct Row16<float> {
+    static constexpr int kN = 4;
+    __device__ static void unpack(const uint4& v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    __device__ static uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    __device__ static float one(float v) { return v; }
+    __device__ static float rounded(float x) { return x; }
+};
+
+// One warp per sorted row; the source rows come from L2 after their first read.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const T* __restrict__ X, int64_t n_tok, int64_t c,
+                                                             int64_t ld, const int* __restrict__ order, int64_t k,
+                                                             int64_t n_rows, T* __restrict__ Xs, int64_t ld_s) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int V = Row16<T>::kN;
+    const int lane = threadIdx.x & 31;
+    const int64_t nv = c / V;
+    for (int64_t p = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); p < n_rows;
+         p += (int64_t)gridDim.x * kRowWarps) {
+        const int64_t f = __ldg(order + p);
+        if (f < 0 || f / k >= n_tok) continue;
+        const T* src = X + (f / k) * ld;
+        T* dst = Xs + p * ld_s;
+        for (int64_t v = lane; v < nv; v += 32)
+            reinterpret_cast<uint4*>(dst)[v] = __ldg(reinterpret_cast<const uint4*>(src) + v);
+        for (int64_t i = nv * V + lane; i < c; i += 32) dst[i] = src[i];
+    }
+}
+
+// One warp per token; the sum runs over the slots in order, in FP32.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restrict__ Ys, int64_t n_rows, int64_t c,
+                                                              int64_t ld_s, const int* __restrict__ pos,
+                                                              const float* __restrict__ w, int64_t n_tok, int k,
+                                                              T* __restrict__ Y, int64_t ld) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int V = Row16<T>::kN;
+    const int lane = threadIdx.x & 31;
+    const int64_t nv = c / V;
+    for (int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); t < n_tok;
+         t += (int64_t)gridDim.x * kRowWarps) {
+        T* dst = Y + t * ld;
+        for (int64_t v = lane; v < nv; v += 32) {
+            float acc[V] = {};
+            for (int s = 0; s < k; ++s) {
+                const int64_t p = __ldg(pos + t * k + s);
+                if (p < 0 || p >= n_rows) continue;
+                const float ws = w ? __ldg(w + t * k + s) : 1.0f;
+                float x[V];
+                Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(Ys + p * ld_s) + v), x);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(ws, x[i], acc[i]);
+            }
+            reinterpret_cast<uint4*>(dst)[v] = Row16<T>::pack(acc);
+        }
+        for (int64_t i = nv * V + lane; i < c; i += 32) {
+            float acc = 0.0f;
+            for (int s = 0; s < k; ++s) {
+                const int64_t p = __ldg(pos + t * k + s);
+                if (p < 0 || p >= n_rows) continue;
+                acc = __fmaf_rn(w ? __ldg(w + t * k + s) : 1.0f, Row16<T>::one(Ys[p * ld_s + i]), acc);
+            }
+            dst[i] = Row16<T>::rounded(acc);
+        }
+    }
+}
+
+// One warp per token: dY[t] times each weight into the sorted rows, and the dot
+// products with the rows, in FP32 in an order fixed by the lanes.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const T* __restrict__ dY, int64_t n_tok, int k,
+                                                                   int64_t c, int64_t ld, const T* __restrict__ Ys,
+                                                                   int64_t ld_s, int64_t n_rows,
+                                                                   const int* __restrict__ pos,
+                                                                   const float* __restrict__ w, T* __restrict__ dYs,
+                                                                   int64_t ld_d, float* __restrict__ dw) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int V = Row16<T>::kN;
+    const int lane = threadIdx.x & 31;
+    const int64_t nv = c / V;
+    for (int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); t < n_tok;
+         t += (int64_t)gridDim.x * kRowWarps) {
+        const T* dy = dY + t * ld;
+        for (int s = 0; s < k; ++s) {
+            const int64_t p = __ldg(pos + t * k + s);
+            float dot = 0.0f;
+            if (p >= 0 && p < n_rows) {
+                const float ws = w ? __ldg(w + t * k + s) : 1.0f;
+                for (int64_t v = lane; v < nv; v += 32) {
+                    float g[V], y[V];
+                    Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(dy) + v), g);
+                    if (dw) {
+                        Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(Ys + p * ld_s) + v), y);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) dot = __fmaf_rn(g[i], y[i], dot);
+                    }
+                    if (dYs) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) g[i] *= ws;
+                        reinterpret_cast<uint4*>(dYs + p * ld_d)[v] = Row16<T>::pack(g);
+                    }
+                }
+                for (int64_t i = nv * V + lane; i < c; i += 32) {
+                    const float g = Row16<T>::one(dy[i]);
+                    if (dw) dot = __fmaf_rn(g, Row16<T>::one(Ys[p * ld_s + i]), dot);
+                    if (dYs) dYs[p * ld_d + i] = Row16<T>::rounded(g * ws);
+                }
+            }
+            if (dw) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+                if (lane == 0) dw[t * k + s] = dot;
+            }
+        }
+    }
+}
+
+unsigned row_grid(int64_t rows, int sms) {
+    const int64_t need = (rows + kRowWarps - 1) / kRowWarps, cap = (int64_t)sms * 8;
+    return (unsigned)(need < cap ? need : cap);
+}
+
+lh_status check_rows(const char* name, const void* p, lh_dtype t, int64_t c, int64_t ld) {
+    if (ld < c) return fail(LH_ERR_INVALID_ARG, "%s: leading dimension %lld < %lld columns", name, (long long)ld, (long long)c);
+    if (!aligned16(p) || (ld * elem_bytes(t)) % 16 != 0)
+        return fail(LH_ERR_ALIGNMENT, "%s must be 16-byte aligned with 16-byte aligned rows", name);
+    return LH_OK;
+}
+
+lh_status check_slots(int64_t n_tok, int64_t k) {
+    if (n_tok < 0 || k < 1) return fail(LH_ERR_INVALID_ARG, "n_tok must be >= 0 and k >= 1");
+    if (k > INT_MAX || (n_tok > 0 && n_tok > INT_MAX / k))
+        return fail(LH_ERR_UNSUPPORTED, "n_tok * k must be below 2^31");
+    return LH_OK;
+}
+
+// Launch with programmatic serialisation: the kernels wait for the one before
+// (griddepcontrol.wait) before they touch memory, so their start-up overlaps its end.
+template <typename... P, typename... A>
+lh_status launch_rows(const char* what, void (*kernel)(P...), unsigned grid, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...), what);
+}
+
+}  // namespace
+}  // namespace lh
+
+extern "C" lh_status lh_route_tokens(const int32_t* ids, int64_t n_tok, int64_t k, int64_t n_experts,
+                                     int64_t* offsets, int32_t* order, int32_t* pos, void* stream) {
+    using namespace lh;
+    clear_error();
+    lh_status s = check_slots(n_tok, k);
+    if (s != LH_OK) return s;
+    if (n_experts < 1) return fail(LH_ERR_INVALID_ARG, "n_experts must be >= 1");
+    if (n_experts > kMaxExperts)
+        return fail(LH_ERR_UNSUPPORTED, "n_experts=%lld is above %d", (long long)n_experts, kMaxExperts);
+    if (!offsets || (n_tok > 0 && (!ids || !order || !pos))) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_tok > 0 && (order == pos || ids == order || ids == pos))
+        return fail(LH_ERR_INVALID_ARG, "order, pos and ids must be different arrays");
+    if (sm_count() <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    const int n = (int)(n_tok * k), E = (int)n_experts;
+    const size_t smem = (size_t)(kRouteWarps + 2) * E * sizeof(uint32_t);
+    if (smem > 48 * 1024) {
+        s = cuda_status(cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                        "route_kernel shared memory");
+        if (s != LH_OK) return s;
+    }
+    // one CTA walks 4096 ids in 4 steps of its warps; more ids want the cluster's eight SMs
+    const unsigned ctas = n <= 4 * kRouteThreads ? 1 : kRouteCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kRouteThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, route_kernel, (const int*)ids, n, E, offsets, (int*)order, (int*)pos),
+                       "route_kernel launch");
+}
+
+extern "C" lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_tok, int64_t c, int64_t ld_x,
+                                      const int32_t* order, int64_t k, int64_t n_rows, void* Xs, int64_t ld_xs,
+                                      void* stream) {
+    using namespace lh;
+    clear_error();
+    if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
+    if (!X || !order || !Xs) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_tok < 0 || c < 0 || k < 1 || n_rows < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, k >= 1");
+    if (X == Xs) return fail(LH_ERR_INVALID_ARG, "Xs must not alias X");
+    lh_status s = check_rows("X", X, dtype, c, ld_x);
+    if (s == LH_OK) s = check_rows("Xs", Xs, dtype, c, ld_xs);
+    if (s != LH_OK) return s;
+    if (n_tok == 0 || c == 0 || n_rows == 0) return LH_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    const unsigned grid = row_grid(n_rows, sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int* o = (const int*)order;
+    if (dtype == LH_BF16)
+        return launch_rows("gather_kernel launch", gather_kernel<uint16_t>, grid, st, (const uint16_t*)X, n_tok, c, ld_x,
+                           o, k, n_rows, (uint16_t*)Xs, ld_xs);
+    return launch_rows("gather_kernel launch", gather_kernel<float>, grid, st, (const float*)X, n_tok, c, ld_x, o, k,
+                       n_rows, (float*)Xs, ld_xs);
+}
+
+extern "C" lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n_rows, int64_t c, int64_t ld_ys,
+                                       const int32_t* pos, const float* weights, int64_t n_tok, int64_t k, void* Y,
+                                       int64_t ld_y, void* stream) {
+    using namespace lh;
+    clear_error();
+    if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
+    lh_status s = check_slots(n_tok, k);
+    if (s != LH_OK) return s;
+    if (!Ys || !pos || !Y) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_rows < 0 || c < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0");
+    if (Y == Ys) return fail(LH_ERR_INVALID_ARG, "Y must not alias Ys");
+    s = check_rows("Ys", Ys, dtype, c, ld_ys);
+    if (s == LH_OK) s = check_rows("Y", Y, dtype, c, ld_y);
+    if (s != LH_OK) return s;
+    if (n_tok == 0 || c == 0) return LH_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    const unsigned grid = row_grid(n_tok, sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == LH_BF16)
+        return launch_rows("combine_kernel launch", combine_kernel<uint16_t>, grid, st, (const uint16_t*)Ys, n_rows, c,
+                           ld_ys, (const int*)pos, weights, n_tok, (int)k, (uint16_t*)Y, ld_y);
+    return launch_rows("combine_kernel launch", combine_kernel<float>, grid, st, (const float*)Ys, n_rows, c, ld_ys,
+                       (const int*)pos, weights, n_tok, (int)k, (float*)Y, ld_y);
+}
+
+extern "C" lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int64_t n_tok, int64_t k, int64_t c,
+                                            int64_t ld_dy, const void* Ys, int64_t ld_ys, int64_t n_rows,
+                                            const int32_t* pos, const float* weights, void* dYs, int64_t ld_dys,
+                                            float* dweights, void* stream) {
+    using namespace lh;
+    clear_error();
+    if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
+    lh_status s = check_slots(n_tok, k);
+    if (s != LH_OK) return s;
+    if (!dY || !pos) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (!dYs && !dweights) return fail(LH_ERR_INVALID_ARG, "one of dYs and dweights is needed");
+    if (dweights && !Ys) return fail(LH_ERR_INVALID_ARG, "dweights needs Ys");
+    if (n_rows < 0 || c < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0");
+    if (dYs == dY || (dYs && dYs == Ys)) return fail(LH_ERR_INVALID_ARG, "dYs must not alias an input");
+    s = check_rows("dY", dY, dtype, c, ld_dy);
+    if (s == LH_OK && dweights) s = check_rows("Ys", Ys, dtype, c, ld_ys);
+    if (s == LH_OK && dYs) s = check_rows("dYs", dYs, dtype, c, ld_dys);
+    if (s != LH_OK) return s;
+    if (n_tok == 0 || (c == 0 && !dweights)) return LH_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    const unsigned grid = row_grid(n_tok, sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == LH_BF16)
+        return launch_rows("combine_grad_kernel launch", combine_grad_kernel<uint16_t>, grid, st, (const uint16_t*)dY,
+                           n_tok, (int)k, c, ld_dy, (const uint16_t*)Ys, ld_ys, n_rows, (const int*)pos, weights,
+                           (uint16_t*)dYs, ld_dys, dweights);
+    return launch_rows("combine_grad_kernel launch", combine_grad_kernel<float>, grid, st, (const float*)dY, n_tok,
+                       (int)k, c, ld_dy, (const float*)Ys, ld_ys, n_rows, (const int*)pos, weights, (float*)dYs, ld_dys,
+                       dweights);
+}

@@ -1,0 +1,465 @@
+// Products of NVFP4 tokens and NVFP4 weights on the block-scaled tensor cores.
+//
+//   Y[t][r] = cast( gx[t] * gw[m] * sum_j vx[t][j] vw[m][r][j] sum_{i in block j} qx[t][i] qw[m][r][i] )
+//
+// for the tokens t of group m (one matrix per group: the experts of a bank, or one
+// matrix and all tokens), with E2M1 values q, E4M3 block scales v and FP32 global
+// scales g: W4A4 inference with the weights that lh_quantize_nvfp4 exports.
+//
+// One warp-specialised CTA per SM walks over output tiles of 128 channels x T tokens:
+// warp 0 fills a ring of stages by TMA (128 bytes = 256 values of each row, and the
+// scale tiles of those columns), warp 1 copies the scales to TMEM and issues
+// tcgen05.mma kind::mxf4nvf4 (K = 64 a step), four warps read the accumulators and
+// store. Channels are the M side, so the N side, the tokens, can be cut to the 16
+// rows that a ragged group's last tile needs.
+#include <climits>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "scale_tiles.cuh"
+#include "tcgen05.cuh"
+
+namespace lh {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128;            // channels of a tile
+constexpr int kStageK = 256;       // columns of a stage: 128 bytes of E2M1 pairs
+constexpr int kRowBytes = kStageK / 2;
+constexpr int kThreads = 192;      // producer, MMA, four epilogue warps
+
+// Set by an expired wait; read and cleared by lh_nvfp4_status.
+__device__ unsigned int product_status;
+
+struct ProdArgs {
+    const int64_t* offsets;  // groups of tokens, or null: one group of all
+    int64_t G, n_rows, c_out, ld_y;
+    int mtiles;              // channel tiles per matrix
+    int stages_k;            // stages along c_in
+    int steps;               // 64-column steps along c_in
+    const uint8_t* xs;       // scale tiles of the tokens
+    const uint8_t* ws;       // scale tiles of the weights
+    const float* xg;         // [n_rows]
+    const float* wg;         // [G]
+    void* Y;
+};
+
+template <int T>
+struct Shape {
+    static constexpr int kScaleTiles = (T + kTileRows - 1) / kTileRows;  // token scale tiles per step
+    static constexpr int kA = kM * kRowBytes, kB = T * kRowBytes;
+    static constexpr int kSa = 4 * kTileBytes, kSb = 4 * kTileBytes * kScaleTiles;
+    static constexpr int kStageBytes = kA + kB + kSa + kSb;
+    static constexpr int kStages = (220 * 1024) / kStageBytes < 8 ? (220 * 1024) / kStageBytes : 8;
+    static constexpr int kAcc = T > 128 ? 1 : 2;                         // accumulators in TMEM
+    static constexpr int kScaleCol = kAcc * T < 32 ? 32 : kAcc * T;      // first TMEM column of the scales
+    static constexpr int kSetCols = 16 + 16 * kScaleTiles;               // scales of one stage
+    static constexpr int kTmemCols = 512;
+    static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "TMEM columns");
+};
+
+template <int T>
+struct Control {
+    uint64_t full[Shape<T>::kStages], empty[Shape<T>::kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+struct Tile {
+    int64_t g, lo, row0;
+    int rows, mt, sub;  // rows left in the group from row0 (at most T); sub: row0 - lo
+};
+
+// Walks over the tiles of all groups in order; every warp of the CTA does so by itself.
+// Groups are looked at 32 at a time, one per lane.
+template <int T>
+struct Walk {
+    int64_t g = 0;
+    int base = 0;  // tiles before group g
+    __device__ void range(const ProdArgs& p, int64_t i, int64_t& lo, int64_t& hi) const {
+        if (!p.offsets) {
+            lo = 0;
+            hi = p.n_rows;
+            return;
+        }
+        lo = __ldg(p.offsets + i);
+        hi = __ldg(p.offsets + i + 1);
+        lo = lo < 0 ? 0 : (lo > p.n_rows ? p.n_rows : lo);
+        hi = hi < 0 ? 0 : (hi > p.n_rows ? p.n_rows : hi);
+    }
+    __device__ bool find(const ProdArgs& p, int u, Tile& t) {
+        const int lane = threadIdx.x & 31;
+        while (g < p.G) {
+            int64_t lo = 0, hi = 0;
+            if (g + lane < p.G) range(p, g + lane, lo, hi);
+            const int nt = hi > lo ? (int)((hi - lo + T - 1) / T) * p.mtiles : 0;
+            int inc = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, base + inc > u);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                base += __shfl_sync(0xFFFFFFFFu, inc - nt, l);
+                g += l;
+                lo = __shfl_sync(0xFFFFFFFFu, lo, l);
+                hi = __shfl_sync(0xFFFFFFFFu, hi, l);
+                const int i = u - base;
+                const int tt = i / p.mtiles;
+                t.g = g;
+                t.lo = lo;
+                t.mt = i - tt * p.mtiles;
+                t.row0 = lo + (int64_t)tt * T;
+                t.sub = (int)(t.row0 - lo);
+                t.rows = hi - t.row0 < T ? (int)(hi - t.row0) : T;
+                return true;
+            }
+            base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            g += 32;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ void give_up(volatile int* flag) {
+    *flag = 1;
+    atomicExch(&product_status, (unsigned)LH_ERR_TIMEOUT);
+}
+
+__device__ __forceinline__ void store_out(float* y, float v) { *y = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+
+template <int T, typename Tout>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                              const __grid_constant__ CUtensorMap xmap,
+                                                              const ProdArgs p) {
+    using S = Shape<T>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Control<T>& C = *reinterpret_cast<Control<T>*>(base_p + S::kStages * S::kStageBytes);
+    const uint32_t ring = smem_u32(base_p);
+    volatile int* abort_flag = &C.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(smem_u32(&C.full[s]), 1);
+            mbar_init(smem_u32(&C.empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&C.tfull[a]), 1);
+            mbar_init(smem_u32(&C.tempty[a]), 4);
+        }
+        mbar_init(smem_u32(&C.drain), 1);
+        C.abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&C.tmem), S::kTmemCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = C.tmem;
+    // everything above overlaps the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    Walk<T> walk;
+    Tile t;
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
+            const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
+            const uint8_t* wsrc = p.ws + (t.g * p.mtiles + t.mt) * (int64_t)p.steps * kTileBytes;
+            const int64_t xt = group_tile(t.lo, t.g) + t.sub / kTileRows;
+            const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
+            for (int ks = 0; ks < p.stages_k; ++ks) {
+                ok = mbar_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
+                if (!ok) break;
+                const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&C.full[stage]);
+                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
+                    mbar_expect_tx(bar, S::kA + S::kB + nk * kTileBytes * (1 + xtiles));
+                    tma_load_2d(a, &wmap, ks * kRowBytes, wrow, bar);
+                    tma_load_2d(b, &xmap, ks * kRowBytes, (int)t.row0, bar);
+                    bulk_load(sa, wsrc + (int64_t)ks * 4 * kTileBytes, nk * kTileBytes, bar);
+                    for (int i = 0; i < xtiles; ++i)
+                        bulk_load(sb + i * 4 * kTileBytes,
+                                  p.xs + ((xt + i) * p.steps + ks * 4) * (int64_t)kTileBytes, nk * kTileBytes, bar);
+                }
+                ++issued;
+                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (!ok) {  // the loads in flight land before the CTA ends
+            give_up(abort_flag);
+            const int n = issued < S::kStages ? (int)issued : S::kStages;
+            for (int i = 0; i < n; ++i) {
+                if (--stage < 0) { stage = S::kStages - 1; phase ^= 1; }
+                int none = 0;
+                mbar_wait(smem_u32(&C.full[stage]), phase, &none);
+            }
+        }
+    } else if (warp == 1) {
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, aphase = 0, set = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
+            ok = mbar_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
+            if (!ok) break;
+            fence_after();
+            const uint32_t n16 = (t.rows + 15) & ~15;
+            // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
+            const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
+            const uint32_t d = tmem + acc * T;
+            const uint32_t sub_col = (t.sub % kTileRows) / 32;
+            const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
+            for (int ks = 0; ks < p.stages_k; ++ks) {
+                ok = mbar_wait(smem_u32(&C.full[stage]), phase, abort_flag);
+                if (!ok) break;
+                fence_after();
+                if (lane == 0) {
+                    const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
+                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
+                    const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                    for (int k = 0; k < nk; ++k) {
+                        tmem_cp_scales(ca + 4 * k, desc_scales(sa + k * kTileBytes));
+                        for (int i = 0; i < xtiles; ++i)
+                            tmem_cp_scales(cb + 4 * (k * S::kScaleTiles + i),
+                                           desc_scales(sb + (i * 4 + k) * kTileBytes));
+                    }
+                    for (int k = 0; k < nk; ++k)
+                        mma_nvfp4(d, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
+                                  cb + 4 * k * S::kScaleTiles + sub_col, (ks | k) ? 1u : 0u);
+                    mma_commit(smem_u32(&C.empty[stage]));
+                    if (ks == p.stages_k - 1) mma_commit(smem_u32(&C.tfull[acc]));
+                }
+                __syncwarp();
+                set ^= 1;
+                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+            }
+            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+        }
+        if (!ok) {  // the products in flight end before the CTA does
+            give_up(abort_flag);
+            if (lane == 0) mma_commit(smem_u32(&C.drain));
+            __syncwarp();
+            int none = 0;
+            mbar_wait(smem_u32(&C.drain), 0, &none);
+        }
+    } else {
+        const int q = warp & 3;  // the TMEM lanes that this warp can read
+        int acc = 0;
+        uint32_t aphase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
+            const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
+            const float gw = __ldg(p.wg + t.g);
+            ok = mbar_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
+            if (!ok) break;
+            fence_after();
+            Tout* y = static_cast<Tout*>(p.Y) + t.row0 * p.ld_y + ch;
+            for (int c = 0; c < t.rows; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * T + c, r);
+                if (ch < p.c_out) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < t.rows)
+                            store_out(y + (int64_t)(c + i) * p.ld_y,
+                                      __uint_as_float(r[i]) * (gw * __ldg(p.xg + t.row0 + c + i)));
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&C.tempty[acc]));
+            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+        }
+        if (!ok) give_up(abort_flag);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// Packed E2M1 rows as bytes: boxes of 128 bytes x `box_rows` rows, 128-byte swizzle.
+bool make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* p, int64_t rows,
+              int64_t row_bytes, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int T, typename Tout>
+lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
+                         const ProdArgs& p, int sms, cudaStream_t st) {
+    using S = Shape<T>;
+    CUtensorMap wmap, xmap;
+    if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T))
+        return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    const int64_t tiles = (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;  // at most
+    if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
+    const size_t smem = (size_t)S::kStages * S::kStageBytes + 1024 + sizeof(Control<T>);
+    static_assert(S::kStages * S::kStageBytes + 1024 + (int)sizeof(Control<T>) <= 227 * 1024, "shared memory");
+    auto kernel = product_kernel<T, Tout>;
+    lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                              "product_kernel shared memory");
+    if (s != LH_OK) return s;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p), "product_kernel launch");
+}
+
+lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets,
+                        int64_t n_groups, int64_t n_rows, int64_t c_out, int64_t c_in, const void* Y, lh_dtype out_dtype,
+                        int64_t ld_y) {
+    if (!valid_dtype(out_dtype)) return fail(LH_ERR_UNSUPPORTED, "out_dtype %d is not LH_BF16 or LH_F32", (int)out_dtype);
+    if (!W_packed || !W_scales || !W_gscale || !Y) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_rows < 0 || c_out < 0 || c_in < 0 || n_groups < 1)
+        return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
+    if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
+    if (c_in % 32 != 0 || c_in == 0)
+        return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a positive multiple of 32", (long long)c_in);
+    if (ld_y < c_out) return fail(LH_ERR_INVALID_ARG, "ld_y=%lld < c_out=%lld", (long long)ld_y, (long long)c_out);
+    if (!aligned16(W_packed) || !aligned16(W_scales) || !aligned16(Y) || (ld_y * elem_bytes(out_dtype)) % 16 != 0)
+        return fail(LH_ERR_ALIGNMENT, "W_packed, W_scales and Y must be 16-byte aligned, with 16-byte aligned rows of Y");
+    // row and column coordinates of the TMA copies are 32-bit
+    if (n_rows > INT_MAX - 512 || c_in > INT_MAX - 512 || (c_out > 0 && n_groups > (INT_MAX - 512) / c_out))
+        return fail(LH_ERR_UNSUPPORTED, "rows, c_in and n_groups * c_out must be below 2^31 - 512");
+    return LH_OK;
+}
+
+}  // namespace
+}  // namespace lh
+
+extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale,
+                                     const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale,
+                                     const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out,
+                                     int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, void* stream) {
+    using namespace lh;
+    clear_error();
+    lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
+    if (s != LH_OK) return s;
+    if (!X_packed || !X_scales || !X_gscale) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(X_packed) || !aligned16(X_scales))
+        return fail(LH_ERR_ALIGNMENT, "X_packed and X_scales must be 16-byte aligned");
+    if (Y == (const void*)X_packed || Y == (const void*)W_packed || Y == (const void*)X_scales ||
+        Y == (const void*)W_scales)
+        return fail(LH_ERR_INVALID_ARG, "Y must not alias an input");
+    if (n_rows == 0 || c_out == 0) return LH_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    auto encode = encode_fn();
+    if (!encode) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    ProdArgs p;
+    p.offsets = offsets; p.G = n_groups; p.n_rows = n_rows; p.c_out = c_out; p.ld_y = ld_y;
+    p.mtiles = (int)((c_out + kM - 1) / kM);
+    p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
+    p.steps = (int)scale_steps(c_in);
+    p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (out_dtype == LH_BF16) return launch_product<128, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
+    return launch_product<128, float>(encode, X_packed, W_packed, c_in, p, sms, st);
+}
+
+namespace lh {
+namespace {
+struct TokenWs {
+    size_t packed, scales, gscale, total;
+};
+size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+TokenWs token_ws(int64_t n_rows, int64_t c_in, int64_t n_groups) {
+    TokenWs w;
+    w.packed = 0;
+    w.scales = up256((size_t)n_rows * (size_t)(c_in / 2));
+    w.gscale = w.scales + up256(lh_nvfp4_token_scale_bytes(n_rows, c_in, n_groups));
+    w.total = w.gscale + up256((size_t)n_rows * sizeof(float));
+    return w;
+}
+}  // namespace
+}  // namespace lh
+
+extern "C" size_t lh_nvfp4_linear_workspace_bytes(int64_t n_rows, int64_t c_in, int64_t n_groups) {
+    if (n_rows < 1 || n_groups < 1 || c_in < 32 || c_in % 32 != 0) return 0;
+    return lh::token_ws(n_rows, c_in, n_groups).total;
+}
+
+extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c_in, int64_t ld_x,
+                                     const int32_t* rows, int64_t row_div, int64_t n_rows, const int64_t* offsets,
+                                     int64_t n_groups, const float* global_amax, const uint8_t* W_packed,
+                                     const uint8_t* W_scales, const float* W_gscale, int64_t c_out, void* Y,
+                                     lh_dtype out_dtype, int64_t ld_y, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    using namespace lh;
+    clear_error();
+    lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
+    if (s != LH_OK) return s;
+    if (X == Y) return fail(LH_ERR_INVALID_ARG, "Y must not alias an input");
+    const size_t need = lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(LH_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(LH_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    if (n_rows == 0 || c_out == 0) return LH_OK;
+    const TokenWs w = token_ws(n_rows, c_in, n_groups);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* packed = ws + w.packed;
+    uint8_t* scales = ws + w.scales;
+    float* gscale = reinterpret_cast<float*>(ws + w.gscale);
+    s = lh_quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
+                           scales, gscale, nullptr, LH_F32, stream);
+    if (s != LH_OK) return s;
+    return lh_nvfp4_matmul(packed, scales, gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in,
+                           Y, out_dtype, ld_y, stream);
+}
+
+extern "C" lh_status lh_nvfp4_status(void* stream) {
+    using namespace lh;
+    clear_error();
+    void* word = nullptr;
+    lh_status s = cuda_status(cudaGetSymbolAddress(&word, product_status), "cudaGetSymbolAddress");
+    if (s != LH_OK) return s;
+    unsigned int v = 0;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = cuda_status(cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, st), "reading the product status");
+    if (s == LH_OK) s = cuda_status(cudaStreamSynchronize(st), "cudaStreamSynchronize");
+    if (s != LH_OK || v == 0) return s;
+    s = cuda_status(cudaMemsetAsync(word, 0, sizeof(v), st), "clearing the product status");
+    if (s != LH_OK) return s;
+    return fail((lh_status)v, "a bounded wait inside the NVFP4 product gave up; its output is incomplete");
+}
