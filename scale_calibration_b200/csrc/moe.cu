@@ -14,6 +14,7 @@
 #include <climits>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace lh {
 namespace {
@@ -25,26 +26,13 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kMaxExperts = 1024;  // one thread per expert in the scan
 constexpr int kRouteCluster = 8;
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+using tc::cluster_rank;
+using tc::cluster_size;
+using tc::cluster_sync;
+
 __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
-    uint32_t a, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::cluster_addr(tc::smem_u32(p), rank)) : "memory");
     return v;
 }
 

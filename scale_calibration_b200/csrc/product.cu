@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ok = mbar_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
                 if (!ok) break;
                 const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t bar = smem_u32(&C.full[stage]);
                     const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
                     mbar_expect_tx(bar, S::kA + S::kB + nk * kTileBytes * (1 + xtiles));
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ok = mbar_wait(smem_u32(&C.full[stage]), phase, abort_flag);
                 if (!ok) break;
                 fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
                     const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
                     const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         if (!ok) {  // the products in flight end before the CTA does
             give_up(abort_flag);
-            if (lane == 0) mma_commit(smem_u32(&C.drain));
+            if (elect_one()) mma_commit(smem_u32(&C.drain));
             __syncwarp();
             int none = 0;
             mbar_wait(smem_u32(&C.drain), 0, &none);
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             for (int c = 0; c < t.rows; c += 32) {
                 uint32_t r[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * T + c, r);
+                tmem_wait32(r);
                 if (ch < p.c_out) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
