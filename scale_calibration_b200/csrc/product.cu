@@ -37,7 +37,8 @@ __device__ unsigned int product_status;
 struct ProdArgs {
     const int64_t* offsets;  // groups of tokens, or null: one group of all
     int64_t G, n_rows, c_out, ld_y;
-    int mtiles;              // channel tiles per matrix
+    int mtiles;              // channel tiles per matrix (of 128, or of 256 for CTA pairs)
+    int mtiles128;           // rows of scale tiles per matrix
     int stages_k;            // stages along c_in
     int steps;               // 64-column steps along c_in
     const uint8_t* xs;       // scale tiles of the tokens
@@ -126,6 +127,10 @@ struct Walk {
     }
 };
 
+// mbar_wait with one answer for the warp: its lanes may see an expired limit apart.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+}
 __device__ __forceinline__ void give_up(volatile int* flag) {
     *flag = 1;
     atomicExch(&product_status, (unsigned)LH_ERR_TIMEOUT);
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int64_t xt = group_tile(t.lo, t.g) + t.sub / kTileRows;
             const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
             for (int ks = 0; ks < p.stages_k; ++ks) {
-                ok = mbar_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
+                ok = warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
                 if (!ok) break;
                 const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
                 if (elect_one()) {
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             for (int i = 0; i < n; ++i) {
                 if (--stage < 0) { stage = S::kStages - 1; phase ^= 1; }
                 int none = 0;
-                mbar_wait(smem_u32(&C.full[stage]), phase, &none);
+                warp_wait(smem_u32(&C.full[stage]), phase, &none);
             }
         }
     } else if (warp == 1) {
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t phase = 0, aphase = 0, set = 0;
         bool ok = true;
         for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
-            ok = mbar_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
+            ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
             if (!ok) break;
             fence_after();
             const uint32_t n16 = (t.rows + 15) & ~15;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t sub_col = (t.sub % kTileRows) / 32;
             const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
             for (int ks = 0; ks < p.stages_k; ++ks) {
-                ok = mbar_wait(smem_u32(&C.full[stage]), phase, abort_flag);
+                ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
                 if (!ok) break;
                 fence_after();
                 if (elect_one()) {
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (elect_one()) mma_commit(smem_u32(&C.drain));
             __syncwarp();
             int none = 0;
-            mbar_wait(smem_u32(&C.drain), 0, &none);
+            warp_wait(smem_u32(&C.drain), 0, &none);
         }
     } else {
         const int q = warp & 3;  // the TMEM lanes that this warp can read
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
             const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
             const float gw = __ldg(p.wg + t.g);
-            ok = mbar_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
+            ok = warp_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
             if (!ok) break;
             fence_after();
             Tout* y = static_cast<Tout*>(p.Y) + t.row0 * p.ld_y + ch;
@@ -289,6 +294,198 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     __syncthreads();
     fence_after();
     if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// ---------------------------------------------------------------- CTA pairs
+//
+// Tiles of 256 channels x 256 tokens, one per pair of CTAs (cta_group::2): each CTA
+// loads its own 128 channels and half of the tokens, so a stage brings 38 KB for
+// 128 x 256 x 256 products where a tile of 128 x 128 brings 36 KB for half of them. The
+// scales of all 256 tokens go to both CTAs. The accumulator takes 256 TMEM columns and
+// the scales 96, which leaves no room for a second one: eight epilogue warps take a
+// whole accumulator into registers and free it before they scale and store.
+
+constexpr int kPairT = 256;
+constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
+constexpr int kPairStages = 5;
+constexpr int kPairA = kM * kRowBytes, kPairB = kPairT / 2 * kRowBytes;
+constexpr int kPairSa = 4 * kTileBytes, kPairSb = 2 * 4 * kTileBytes;
+constexpr int kPairStageBytes = kPairA + kPairB + kPairSa + kPairSb;
+constexpr int kPairScaleCol = kPairT, kPairSetCols = 16 + 32;
+
+constexpr int kPairRows = 256;  // rows per group from which the pairs are taken
+
+struct PairControl {
+    uint64_t full[kPairStages], empty[kPairStages], tfull, tempty, drain;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <typename Tout>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    product_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                        const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
+                        const ProdArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PairControl& C = *reinterpret_cast<PairControl*>(base_p + kPairStages * kPairStageBytes);
+    const uint32_t ring = smem_u32(base_p);
+    volatile int* abort_flag = &C.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(smem_u32(&C.full[s]), 1);
+            mbar_init(smem_u32(&C.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&C.tfull), 1);
+        mbar_init(smem_u32(&C.tempty), 16);  // the epilogue warps of both CTAs
+        mbar_init(smem_u32(&C.drain), 1);
+        C.abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&C.tmem), 512);
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // the barriers of both CTAs are ready
+    fence_after();
+    const uint32_t tmem = C.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    Walk<kPairT> walk;
+    Tile t;
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int u = first; ok && walk.find(p, u, t); u += step) {
+            const int half = ((t.rows + 15) & ~15) / 2;  // tokens that each CTA brings
+            const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * 2 * kM + rank * kM);
+            const int xrow = (int)t.row0 + (int)rank * half;
+            const int wsrow = (int)((t.g * p.mtiles128 + t.mt * 2 + rank) * p.steps);
+            const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
+            for (int ks = 0; ks < p.stages_k; ++ks) {
+                ok = warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = cluster_addr(smem_u32(&C.full[stage]), 0);
+                    const uint32_t a = ring + stage * kPairStageBytes, b = a + kPairA, sa = b + kPairB, sb = sa + kPairSa;
+                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), 2 * kPairStageBytes);
+                    tma_load_2d_pair(a, &wmap, ks * kRowBytes, wrow, bar);
+                    tma_load_2d_pair(b, &xmap, ks * kRowBytes, xrow, bar);
+                    // past the last step or tile these bring other scales, or zeros, that no product uses
+                    tma_load_2d_pair(sa, &wsmap, 0, wsrow + 4 * ks, bar);
+                    tma_load_2d_pair(sb, &xsmap, 0, xsrow + 4 * ks, bar);
+                    tma_load_2d_pair(sb + 4 * kTileBytes, &xsmap, 0, xsrow + p.steps + 4 * ks, bar);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (!ok) {  // the loads in flight land before the CTAs end (both report to the first one's barriers)
+            give_up(abort_flag);
+            const int n = rank == 0 ? (issued < kPairStages ? (int)issued : kPairStages) : 0;
+            for (int i = 0; i < n; ++i) {
+                if (--stage < 0) { stage = kPairStages - 1; phase ^= 1; }
+                int none = 0;
+                warp_wait(smem_u32(&C.full[stage]), phase, &none);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0, aphase = 0, set = 0;
+            bool ok = true;
+            for (int u = first; ok && walk.find(p, u, t); u += step) {
+                ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
+                if (!ok) break;
+                fence_after();
+                const uint32_t n16 = (t.rows + 15) & ~15;
+                const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
+                for (int ks = 0; ks < p.stages_k; ++ks) {
+                    ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+                        const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
+                        const uint32_t a = ring + stage * kPairStageBytes, b = a + kPairA, sa = b + kPairB,
+                                       sb = sa + kPairSa;
+                        const uint32_t ca = tmem + kPairScaleCol + set * kPairSetCols, cb = ca + 16;
+                        for (int k = 0; k < nk; ++k) {
+                            tmem_cp_scales_pair(ca + 4 * k, desc_scales(sa + k * kTileBytes));
+                            tmem_cp_scales_pair(cb + 8 * k, desc_scales(sb + k * kTileBytes));
+                            tmem_cp_scales_pair(cb + 8 * k + 4, desc_scales(sb + (4 + k) * kTileBytes));
+                        }
+                        for (int k = 0; k < nk; ++k)
+                            mma_nvfp4_pair(tmem, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
+                                           cb + 8 * k, (ks | k) ? 1u : 0u);
+                        mma_commit_pair(smem_u32(&C.empty[stage]));
+                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
+                    }
+                    __syncwarp();
+                    set ^= 1;
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                }
+                aphase ^= 1;
+            }
+            if (!ok) {  // the products in flight end before the CTAs do
+                give_up(abort_flag);
+                if (elect_one()) mma_commit_pair(smem_u32(&C.drain));
+                __syncwarp();
+                int none = 0;
+                warp_wait(smem_u32(&C.drain), 0, &none);
+            }
+        }
+    } else {
+        const int q = warp & 3;           // the TMEM lanes that this warp can read
+        const int h = (warp - 2) >> 2;    // its half of the tokens
+        const uint32_t tempty = cluster_addr(smem_u32(&C.tempty), 0);
+        uint32_t aphase = 0;
+        bool ok = true;
+        for (int u = first; ok && walk.find(p, u, t); u += step) {
+            const int64_t ch = (int64_t)t.mt * 2 * kM + rank * kM + q * 32 + lane;
+            const float gw = __ldg(p.wg + t.g);
+            const int c0 = h * 128, n = t.rows - c0;  // tokens of this warp, if above 0 (128 at most)
+            float gx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                gx[j] = 32 * j + lane < n ? gw * __ldg(p.xg + t.row0 + c0 + 32 * j + lane) : 0.0f;
+            ok = warp_wait(smem_u32(&C.tfull), aphase, abort_flag);
+            if (!ok) break;
+            fence_after();
+            uint32_t r[4][32];
+            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + c0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (32 * j < n) tmem_ld32(src + 32 * j, r[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty);
+            aphase ^= 1;
+            Tout* y = static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y + ch;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float s = __shfl_sync(0xFFFFFFFFu, gx[j], i);
+                    if (32 * j + i < n && ch < p.c_out)
+                        store_out(y + (int64_t)(32 * j + i) * p.ld_y, __uint_as_float(r[j][i]) * s);
+                }
+            }
+        }
+        if (!ok) give_up(abort_flag);
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // nothing of the pair is in flight to either CTA
+    fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -345,6 +542,53 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p), "product_kernel launch");
 }
 
+// Scale tiles as rows of 512 bytes: boxes of the four steps of a stage.
+bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* p, int64_t tiles) {
+    const cuuint64_t dims[2] = {kTileBytes / 4, (cuuint64_t)tiles};
+    const cuuint64_t strides[1] = {kTileBytes};
+    const cuuint32_t box[2] = {kTileBytes / 4, 4};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Tout>
+lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
+                      ProdArgs p, int sms, cudaStream_t st) {
+    p.mtiles = (p.mtiles128 + 1) / 2;
+    const int64_t tiles = (p.offsets ? p.n_rows / kPairT + p.G : (p.n_rows + kPairT - 1) / kPairT) * p.mtiles;
+    const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
+    if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
+        return fail(LH_ERR_UNSUPPORTED, "too many tiles");
+    CUtensorMap wmap, xmap, wsmap, xsmap;
+    if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kPairT / 2) ||
+        !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
+        return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    constexpr size_t smem = (size_t)kPairStages * kPairStageBytes + 1024 + sizeof(PairControl);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    auto kernel = product_pair_kernel<Tout>;
+    lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                              "product_pair_kernel shared memory");
+    if (s != LH_OK) return s;
+    const int64_t pairs = sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_pair_kernel launch");
+}
+
 lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets,
                         int64_t n_groups, int64_t n_rows, int64_t c_out, int64_t c_in, const void* Y, lh_dtype out_dtype,
                         int64_t ld_y) {
@@ -388,11 +632,15 @@ extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_s
     if (!encode) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     ProdArgs p;
     p.offsets = offsets; p.G = n_groups; p.n_rows = n_rows; p.c_out = c_out; p.ld_y = ld_y;
-    p.mtiles = (int)((c_out + kM - 1) / kM);
+    p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
     p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
     p.steps = (int)scale_steps(c_in);
     p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n_rows >= kPairRows * n_groups) {
+        if (out_dtype == LH_BF16) return launch_pair<__nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
+        return launch_pair<float>(encode, X_packed, W_packed, c_in, p, sms, st);
+    }
     if (out_dtype == LH_BF16) return launch_product<128, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
     return launch_product<128, float>(encode, X_packed, W_packed, c_in, p, sms, st);
 }
