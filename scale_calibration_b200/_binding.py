@@ -95,10 +95,22 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_torch = None  # torch, imported when a tensor or the current stream is first needed
+_DTYPES: dict = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _DTYPES.update({torch.bfloat16: LH_BF16, torch.float32: LH_F32})
+    _torch = torch
+    return torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        t = _torch or _load_torch()
+        return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -107,12 +119,12 @@ def _stream(stream) -> int | None:
 def _dtype(t) -> int:
     if isinstance(t, int):
         return t
-    import torch
-    if t.dtype == torch.bfloat16:
-        return LH_BF16
-    if t.dtype == torch.float32:
-        return LH_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    if _torch is None:
+        _load_torch()
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return d
 
 
 def _check(status: int, where: str) -> None:

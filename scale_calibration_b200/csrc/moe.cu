@@ -139,7 +139,6 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __re
 // ---------------------------------------------------------------- rows
 
 constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
 
 template <typename T>
 struct Row16;  // 16 bytes of a row as floats
@@ -180,28 +179,61 @@ struct Row16<float> {
     __device__ static float rounded(float x) { return x; }
 };
 
-// One warp per sorted row; the source rows come from L2 after their first read.
+// Rows are worked on as 16-byte vectors, one thread per vector of a row (gather: of
+// kGatherRows rows), flat over the rows: neighbouring threads take neighbouring vectors,
+// a few rows fill as many threads as they can, and every thread has its rows' loads in
+// flight at once. The columns past the last whole vector go one by one to the thread
+// after it.
+constexpr int kGatherRows = 4;
+constexpr int kSlots = 4;  // slots whose rows are loaded together
+
+// This thread's (row, vector) with `per` vectors a row: a 64-bit division for the CTA's
+// first vector, the same in all its threads, and a 32-bit one for each thread.
+__device__ __forceinline__ void split(int64_t first, uint32_t per, int64_t& row, uint32_t& v) {
+    const int64_t row0 = first / per;
+    const uint32_t i = (uint32_t)(first - row0 * per) + threadIdx.x;
+    const uint32_t r = i / per;
+    row = row0 + r;
+    v = i - r * per;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T* __restrict__ X, int64_t n_tok, int64_t c,
                                                              int64_t ld, const int* __restrict__ order, int64_t k,
                                                              int64_t n_rows, T* __restrict__ Xs, int64_t ld_s) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int V = Row16<T>::kN;
-    const int lane = threadIdx.x & 31;
-    const int64_t nv = c / V;
-    for (int64_t p = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); p < n_rows;
-         p += (int64_t)gridDim.x * kRowWarps) {
-        const int64_t f = __ldg(order + p);
-        if (f < 0 || f / k >= n_tok) continue;
-        const T* src = X + (f / k) * ld;
-        T* dst = Xs + p * ld_s;
-        for (int64_t v = lane; v < nv; v += 32)
-            reinterpret_cast<uint4*>(dst)[v] = __ldg(reinterpret_cast<const uint4*>(src) + v);
-        for (int64_t i = nv * V + lane; i < c; i += 32) dst[i] = src[i];
+    const uint32_t nv = (uint32_t)(c / V), per = (uint32_t)((c + V - 1) / V);
+    const int64_t n = (n_rows + kGatherRows - 1) / kGatherRows * per;
+    for (int64_t i = (int64_t)blockIdx.x * kRowThreads; i < n; i += (int64_t)gridDim.x * kRowThreads) {
+        int64_t p0;
+        uint32_t v;
+        split(i, per, p0, v);
+        p0 *= kGatherRows;
+        int64_t t[kGatherRows];
+#pragma unroll
+        for (int r = 0; r < kGatherRows; ++r) {
+            const int f = p0 + r < n_rows ? __ldg(order + p0 + r) : -1;
+            t[r] = f < 0 ? -1 : (int64_t)((uint32_t)f / (uint32_t)k);
+            if (t[r] >= n_tok) t[r] = -1;
+        }
+        if (v < nv) {
+            uint4 x[kGatherRows];
+#pragma unroll
+            for (int r = 0; r < kGatherRows; ++r)
+                if (t[r] >= 0) x[r] = __ldg(reinterpret_cast<const uint4*>(X + t[r] * ld) + v);
+#pragma unroll
+            for (int r = 0; r < kGatherRows; ++r)
+                if (t[r] >= 0) reinterpret_cast<uint4*>(Xs + (p0 + r) * ld_s)[v] = x[r];
+        } else {
+            for (int r = 0; r < kGatherRows; ++r)
+                if (t[r] >= 0)
+                    for (int64_t j = (int64_t)nv * V; j < c; ++j) Xs[(p0 + r) * ld_s + j] = X[t[r] * ld + j];
+        }
     }
 }
 
-// One warp per token; the sum runs over the slots in order, in FP32.
+// The sum runs over the slots in order, in FP32.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restrict__ Ys, int64_t n_rows, int64_t c,
                                                               int64_t ld_s, const int* __restrict__ pos,
@@ -209,92 +241,144 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restric
                                                               T* __restrict__ Y, int64_t ld) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int V = Row16<T>::kN;
-    const int lane = threadIdx.x & 31;
-    const int64_t nv = c / V;
-    for (int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); t < n_tok;
-         t += (int64_t)gridDim.x * kRowWarps) {
-        T* dst = Y + t * ld;
-        for (int64_t v = lane; v < nv; v += 32) {
-            float acc[V] = {};
-            for (int s = 0; s < k; ++s) {
-                const int64_t p = __ldg(pos + t * k + s);
-                if (p < 0 || p >= n_rows) continue;
-                const float ws = w ? __ldg(w + t * k + s) : 1.0f;
-                float x[V];
-                Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(Ys + p * ld_s) + v), x);
+    const uint32_t nv = (uint32_t)(c / V), per = (uint32_t)((c + V - 1) / V);
+    for (int64_t i = (int64_t)blockIdx.x * kRowThreads; i < n_tok * per; i += (int64_t)gridDim.x * kRowThreads) {
+        int64_t t;
+        uint32_t v;
+        split(i, per, t, v);
+        if (t >= n_tok) continue;
+        float acc[V] = {};
+        for (int s0 = 0; s0 < k; s0 += kSlots) {
+            int64_t p[kSlots];
+            float ws[kSlots];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(ws, x[i], acc[i]);
+            for (int s = 0; s < kSlots; ++s) {
+                p[s] = s0 + s < k ? __ldg(pos + t * k + s0 + s) : -1;
+                if (p[s] >= n_rows) p[s] = -1;
+                ws[s] = p[s] >= 0 && w ? __ldg(w + t * k + s0 + s) : 1.0f;
             }
-            reinterpret_cast<uint4*>(dst)[v] = Row16<T>::pack(acc);
+            if (v < nv) {
+                uint4 x[kSlots];
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s)
+                    if (p[s] >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(Ys + p[s] * ld_s) + v);
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (p[s] < 0) continue;
+                    float f[V];
+                    Row16<T>::unpack(x[s], f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = __fmaf_rn(ws[s], f[j], acc[j]);
+                }
+            } else {
+                for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (p[s] >= 0 && (int64_t)nv * V + j < c)
+                            acc[j] = __fmaf_rn(ws[s], Row16<T>::one(Ys[p[s] * ld_s + (int64_t)nv * V + j]), acc[j]);
+            }
         }
-        for (int64_t i = nv * V + lane; i < c; i += 32) {
-            float acc = 0.0f;
-            for (int s = 0; s < k; ++s) {
-                const int64_t p = __ldg(pos + t * k + s);
-                if (p < 0 || p >= n_rows) continue;
-                acc = __fmaf_rn(w ? __ldg(w + t * k + s) : 1.0f, Row16<T>::one(Ys[p * ld_s + i]), acc);
-            }
-            dst[i] = Row16<T>::rounded(acc);
+        T* dst = Y + t * ld;
+        if (v < nv) {
+            reinterpret_cast<uint4*>(dst)[v] = Row16<T>::pack(acc);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if ((int64_t)nv * V + j < c) dst[(int64_t)nv * V + j] = Row16<T>::rounded(acc[j]);
         }
     }
 }
 
-// One warp per token: dY[t] times each weight into the sorted rows, and the dot
-// products with the rows, in FP32 in an order fixed by the lanes.
+// One CTA per token, kSlots slots at a time: dY[t] times each weight into the sorted
+// rows, and the dot products with the rows, in FP32 in an order fixed by the threads.
+constexpr int kGradThreads = 128;
+
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const T* __restrict__ dY, int64_t n_tok, int k,
-                                                                   int64_t c, int64_t ld, const T* __restrict__ Ys,
-                                                                   int64_t ld_s, int64_t n_rows,
-                                                                   const int* __restrict__ pos,
-                                                                   const float* __restrict__ w, T* __restrict__ dYs,
-                                                                   int64_t ld_d, float* __restrict__ dw) {
+__global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const T* __restrict__ dY, int64_t n_tok, int k,
+                                                                    int64_t c, int64_t ld, const T* __restrict__ Ys,
+                                                                    int64_t ld_s, int64_t n_rows,
+                                                                    const int* __restrict__ pos,
+                                                                    const float* __restrict__ w, T* __restrict__ dYs,
+                                                                    int64_t ld_d, float* __restrict__ dw) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int V = Row16<T>::kN;
-    const int lane = threadIdx.x & 31;
+    __shared__ float part[kGradThreads / 32][kSlots];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t nv = c / V;
-    for (int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); t < n_tok;
-         t += (int64_t)gridDim.x * kRowWarps) {
+    for (int64_t t = blockIdx.x; t < n_tok; t += gridDim.x) {
         const T* dy = dY + t * ld;
-        for (int s = 0; s < k; ++s) {
-            const int64_t p = __ldg(pos + t * k + s);
-            float dot = 0.0f;
-            if (p >= 0 && p < n_rows) {
-                const float ws = w ? __ldg(w + t * k + s) : 1.0f;
-                for (int64_t v = lane; v < nv; v += 32) {
-                    float g[V], y[V];
-                    Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(dy) + v), g);
-                    if (dw) {
-                        Row16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(Ys + p * ld_s) + v), y);
+        for (int s0 = 0; s0 < k; s0 += kSlots) {
+            int64_t p[kSlots];
+            float ws[kSlots], dot[kSlots] = {};
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot = __fmaf_rn(g[i], y[i], dot);
+            for (int s = 0; s < kSlots; ++s) {
+                p[s] = s0 + s < k ? __ldg(pos + t * k + s0 + s) : -1;
+                if (p[s] >= n_rows) p[s] = -1;
+                ws[s] = p[s] >= 0 && w ? __ldg(w + t * k + s0 + s) : 1.0f;
+            }
+            for (int64_t v = tid; v < nv; v += kGradThreads) {
+                uint4 x[kSlots];
+                const uint4 gv = __ldg(reinterpret_cast<const uint4*>(dy) + v);
+                if (dw) {
+#pragma unroll
+                    for (int s = 0; s < kSlots; ++s)
+                        if (p[s] >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(Ys + p[s] * ld_s) + v);
+                }
+                float g[V];
+                Row16<T>::unpack(gv, g);
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (p[s] < 0) continue;
+                    if (dw) {
+                        float y[V];
+                        Row16<T>::unpack(x[s], y);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) dot[s] = __fmaf_rn(g[j], y[j], dot[s]);
                     }
                     if (dYs) {
+                        float d[V];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) g[i] *= ws;
-                        reinterpret_cast<uint4*>(dYs + p * ld_d)[v] = Row16<T>::pack(g);
+                        for (int j = 0; j < V; ++j) d[j] = g[j] * ws[s];
+                        reinterpret_cast<uint4*>(dYs + p[s] * ld_d)[v] = Row16<T>::pack(d);
                     }
                 }
-                for (int64_t i = nv * V + lane; i < c; i += 32) {
-                    const float g = Row16<T>::one(dy[i]);
-                    if (dw) dot = __fmaf_rn(g, Row16<T>::one(Ys[p * ld_s + i]), dot);
-                    if (dYs) dYs[p * ld_d + i] = Row16<T>::rounded(g * ws);
+            }
+            for (int64_t j = nv * V + tid; j < c; j += kGradThreads) {
+                const float g = Row16<T>::one(dy[j]);
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (p[s] < 0) continue;
+                    if (dw) dot[s] = __fmaf_rn(g, Row16<T>::one(Ys[p[s] * ld_s + j]), dot[s]);
+                    if (dYs) dYs[p[s] * ld_d + j] = Row16<T>::rounded(g * ws[s]);
                 }
             }
-            if (dw) {
+            if (!dw) continue;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-                if (lane == 0) dw[t * k + s] = dot;
+            for (int s = 0; s < kSlots; ++s) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dot[s] += __shfl_xor_sync(0xFFFFFFFFu, dot[s], o);
+                if (lane == 0) part[tid >> 5][s] = dot[s];
             }
+            __syncthreads();
+            if (tid < kSlots && s0 + tid < k) {
+                float d = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kGradThreads / 32; ++i) d += part[i][tid];
+                dw[t * k + s0 + tid] = d;
+            }
+            __syncthreads();
         }
     }
 }
 
-unsigned row_grid(int64_t rows, int sms) {
-    const int64_t need = (rows + kRowWarps - 1) / kRowWarps, cap = (int64_t)sms * 8;
+// CTAs for `items` of `per_cta`, at most `waves` CTAs per SM.
+unsigned grid_for(int64_t items, int64_t per_cta, int sms, int waves) {
+    const int64_t need = (items + per_cta - 1) / per_cta, cap = (int64_t)sms * waves;
     return (unsigned)(need < cap ? need : cap);
 }
 
 lh_status check_rows(const char* name, const void* p, lh_dtype t, int64_t c, int64_t ld) {
+    if (c > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "rows must have fewer than 2^31 columns");
     if (ld < c) return fail(LH_ERR_INVALID_ARG, "%s: leading dimension %lld < %lld columns", name, (long long)ld, (long long)c);
     if (!aligned16(p) || (ld * elem_bytes(t)) % 16 != 0)
         return fail(LH_ERR_ALIGNMENT, "%s must be 16-byte aligned with 16-byte aligned rows", name);
@@ -311,10 +395,10 @@ lh_status check_slots(int64_t n_tok, int64_t k) {
 // Launch with programmatic serialisation: the kernels wait for the one before
 // (griddepcontrol.wait) before they touch memory, so their start-up overlaps its end.
 template <typename... P, typename... A>
-lh_status launch_rows(const char* what, void (*kernel)(P...), unsigned grid, cudaStream_t st, A... args) {
+lh_status launch_rows(const char* what, void (*kernel)(P...), unsigned grid, int threads, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -381,13 +465,14 @@ extern "C" lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_t
     if (n_tok == 0 || c == 0 || n_rows == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const unsigned grid = row_grid(n_rows, sms);
+    const int64_t per = (c * elem_bytes(dtype) + 15) / 16;
+    const unsigned grid = grid_for((n_rows + kGatherRows - 1) / kGatherRows * per, kRowThreads, sms, 32);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int* o = (const int*)order;
     if (dtype == LH_BF16)
-        return launch_rows("gather_kernel launch", gather_kernel<uint16_t>, grid, st, (const uint16_t*)X, n_tok, c, ld_x,
+        return launch_rows("gather_kernel launch", gather_kernel<uint16_t>, grid, kRowThreads, st, (const uint16_t*)X, n_tok, c, ld_x,
                            o, k, n_rows, (uint16_t*)Xs, ld_xs);
-    return launch_rows("gather_kernel launch", gather_kernel<float>, grid, st, (const float*)X, n_tok, c, ld_x, o, k,
+    return launch_rows("gather_kernel launch", gather_kernel<float>, grid, kRowThreads, st, (const float*)X, n_tok, c, ld_x, o, k,
                        n_rows, (float*)Xs, ld_xs);
 }
 
@@ -408,12 +493,12 @@ extern "C" lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n
     if (n_tok == 0 || c == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const unsigned grid = row_grid(n_tok, sms);
+    const unsigned grid = grid_for(n_tok * ((c * elem_bytes(dtype) + 15) / 16), kRowThreads, sms, 32);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == LH_BF16)
-        return launch_rows("combine_kernel launch", combine_kernel<uint16_t>, grid, st, (const uint16_t*)Ys, n_rows, c,
+        return launch_rows("combine_kernel launch", combine_kernel<uint16_t>, grid, kRowThreads, st, (const uint16_t*)Ys, n_rows, c,
                            ld_ys, (const int*)pos, weights, n_tok, (int)k, (uint16_t*)Y, ld_y);
-    return launch_rows("combine_kernel launch", combine_kernel<float>, grid, st, (const float*)Ys, n_rows, c, ld_ys,
+    return launch_rows("combine_kernel launch", combine_kernel<float>, grid, kRowThreads, st, (const float*)Ys, n_rows, c, ld_ys,
                        (const int*)pos, weights, n_tok, (int)k, (float*)Y, ld_y);
 }
 
@@ -438,13 +523,13 @@ extern "C" lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int6
     if (n_tok == 0 || (c == 0 && !dweights)) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const unsigned grid = row_grid(n_tok, sms);
+    const unsigned grid = grid_for(n_tok, 1, sms, 64);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == LH_BF16)
-        return launch_rows("combine_grad_kernel launch", combine_grad_kernel<uint16_t>, grid, st, (const uint16_t*)dY,
+        return launch_rows("combine_grad_kernel launch", combine_grad_kernel<uint16_t>, grid, kGradThreads, st, (const uint16_t*)dY,
                            n_tok, (int)k, c, ld_dy, (const uint16_t*)Ys, ld_ys, n_rows, (const int*)pos, weights,
                            (uint16_t*)dYs, ld_dys, dweights);
-    return launch_rows("combine_grad_kernel launch", combine_grad_kernel<float>, grid, st, (const float*)dY, n_tok,
+    return launch_rows("combine_grad_kernel launch", combine_grad_kernel<float>, grid, kGradThreads, st, (const float*)dY, n_tok,
                        (int)k, c, ld_dy, (const float*)Ys, ld_ys, n_rows, (const int*)pos, weights, (float*)dYs, ld_dys,
                        dweights);
 }
