@@ -458,6 +458,7 @@ extern "C" lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_t
     if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
     if (!X || !order || !Xs) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_tok < 0 || c < 0 || k < 1 || n_rows < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, k >= 1");
+    if (k > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "k must be below 2^31");
     if (X == Xs) return fail(LH_ERR_INVALID_ARG, "Xs must not alias X");
     lh_status s = check_rows("X", X, dtype, c, ld_x);
     if (s == LH_OK) s = check_rows("Xs", Xs, dtype, c, ld_xs);

@@ -15,102 +15,254 @@
 namespace lh {
 namespace {
 
-constexpr int kTokThreads = 256;
+// Blocks that a thread keeps in registers between the two passes (32 registers).
+template <typename T>
+constexpr int kHeld = 8 / (int)sizeof(T);
 
 struct TokenArgs {
-    int64_t n_src, ld, row_div, n_rows, G, J, steps;
+    int64_t n_src, ld, n_rows, G, J, steps;
+    uint32_t row_div;
     const int* rows;         // source of each row (over row_div), or null
     const int64_t* offsets;  // groups of rows, or null
     const float* gamax;      // amax of the tensor, or null (per token)
+    bool wide_in, wide_out;  // rows of X, X_out 32-byte aligned
     uint8_t* packed;
     uint8_t* tiles;
     float* gscale;
 };
 
-// Largest group g with offsets[g] <= row; false when the row lies in no group.
+// Largest group g with offsets[g] <= row, by the whole warp, 32 offsets a round; false
+// when the row lies in no group.
 __device__ __forceinline__ bool find_group(const TokenArgs& p, int64_t row, int64_t& g, int64_t& lo) {
-    if (!p.offsets) {
-        g = 0;
-        lo = 0;
-        return true;
+    g = 0;
+    lo = 0;
+    if (!p.offsets) return true;
+    const int lane = threadIdx.x & 31;
+    int64_t span = p.G;  // offsets[g] <= row < offsets[g + span], if there is such a group
+    while (span > 1) {
+        const int64_t step = (span + 31) / 32;
+        const bool le = lane * step < span && __ldg(p.offsets + g + lane * step) <= row;
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, le);
+        const int l = hit ? 31 - __clz(hit) : 0;
+        g += l * step;
+        span = span - l * step < step ? span - l * step : step;
     }
-    int64_t a = 0, b = p.G;  // offsets[a] <= row < offsets[b] if there is such a group
-    while (b - a > 1) {
-        const int64_t m = (a + b) >> 1;
-        if (__ldg(p.offsets + m) <= row) a = m; else b = m;
-    }
-    g = a;
-    lo = __ldg(p.offsets + a);
+    lo = __ldg(p.offsets + g);
     lo = lo < 0 ? 0 : lo;
-    return lo <= row && row < __ldg(p.offsets + a + 1);
+    return lo <= row && row < __ldg(p.offsets + g + 1);
 }
 
-__device__ __forceinline__ uint32_t block_max_bits(const float (&w)[16]) {
-    uint32_t m = 0;  // as integers, infinities and NaN come out on top
+// 16 values as they lie in memory.
+template <typename T>
+struct Held {
+    uint32_t v[8 * (sizeof(T) / 2)];
+    // wide: p is 32-byte aligned. A warp's 32-byte accesses fill whole sectors, where 16
+    // bytes of every 32 or 64 make L2 handle each sector twice.
+    __device__ void load(const T* p, bool wide) {
+        if (wide) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(w[i]) & 0x7FFFFFFFu);
-    return m;
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                uint32_t* u = v + 8 * i;
+                asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                    : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                    : "l"(reinterpret_cast<const uint32_t*>(p) + 8 * i));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+            }
+        }
+    }
+    __device__ void floats(float (&w)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                w[2 * i] = __uint_as_float(v[i] << 16);
+                w[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+            } else {
+                w[2 * i] = __uint_as_float(v[2 * i]);
+                w[2 * i + 1] = __uint_as_float(v[2 * i + 1]);
+            }
+        }
+    }
+    // Bits of the largest |x|; as integers, infinities and NaN come out on top.
+    __device__ uint32_t max_bits() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(T) == 2) {  // two bf16 at a time
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+            return max(m << 16, m & 0xFFFF0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = max(m, v[i] & 0x7FFFFFFFu);
+            return m;
+        }
+    }
+};
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+__device__ __forceinline__ void store16(uint16_t* p, const float (&o)[16], bool wide) {
+    if (!wide) return Vec16<uint16_t>::store(p, o);
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    store32(p, u);
+}
+__device__ __forceinline__ void store16(float* p, const float (&o)[16], bool wide) {
+    if (!wide) return Vec16<float>::store(p, o);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(o[8 * i + j]);
+        store32(p + 8 * i, u);
+    }
 }
 
-// One CTA per row: the row's largest |x|, then its blocks (from registers when a
-// thread has one block at most, else read again, from L1 or L2).
-template <typename Tin, typename Tout, bool kOut>
-__global__ void __launch_bounds__(kTokThreads) tokens_kernel(const Tin* __restrict__ X, TokenArgs p,
-                                                             Tout* __restrict__ out) {
+// A row's global scale, with its reciprocal where the quotient of a block needs no
+// division: with g in [2^-85, 2^100], q = RN(a y) and RN(q + (a - q g) y) with y = RN(1/g)
+// is the correctly rounded a / g for |a| >= 2^-100 (P. Markstein, IBM J. Res. Dev. 34(1),
+// 1990: the residual is exact), and a smaller a gives less than 2^-14 either way, code 1.
+// The same holds for a / 6.
+struct RowScale {
+    float g, ny, nan;
+    bool fast;
+    __device__ explicit RowScale(float gs) {
+        g = gs;
+        nan = __int_as_float(0x7FFFFFFF);
+        fast = gs >= 2.584939e-26f && gs <= 1.2676506e30f;
+        ny = fast ? -__frcp_rn(gs) : 0.0f;
+    }
+    __device__ static float quotient(float a, float d, float nyd) {
+        const float nq = __fmul_rn(a, nyd);          // -q
+        const float r = __fmaf_rn(nq, d, a);         // a - q d
+        return -__fmaf_rn(r, nyd, nq);
+    }
+    // E4M3 code of a block whose largest |x| is a, and the block's scale.
+    __device__ uint32_t code(float a, float& s) const {
+        uint32_t c = 1;
+        if (fast)
+            c = (uint32_t)e4m3_rne_code(quotient(quotient(a, 6.0f, -0.16666667f), g, ny));
+        else if (g != 0.0f)
+            c = (uint32_t)e4m3_rne_code(__fdiv_rn(__fdiv_rn(a, 6.0f), g));
+        c = c < 1 ? 1 : c;
+        uint32_t h2;  // the code's value, exact in f16
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
+        s = __fmul_rn(__low2float(*reinterpret_cast<const __half2*>(&h2)), g);
+        return c;
+    }
+};
+
+// kWarps warps per row. With the token's own scale each thread loads its blocks of the
+// row and keeps them, the warps agree on the row's largest |x|, and the blocks are
+// quantised from the registers; rows too wide for that are read twice (from L2). With a
+// given scale one pass does.
+template <typename Tin, typename Tout, bool kOut, int kWarps>
+__global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
+    tokens_kernel(const Tin* __restrict__ X, TokenArgs p, Tout* __restrict__ out) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ uint32_t red[kTokThreads / 32];
-    const int tid = threadIdx.x;
-    for (int64_t row = blockIdx.x; row < p.n_rows; row += gridDim.x) {
+    constexpr int kRows = 8 / kWarps;   // rows of a CTA
+    constexpr int kSpan = 32 * kWarps;  // threads of a row
+    constexpr int kN = kHeld<Tin>;
+    __shared__ uint32_t red[kRows][kWarps];
+    const int tid = threadIdx.x % kSpan, part = threadIdx.x / kSpan, warp = tid >> 5, lane = tid & 31;
+    const int J = (int)p.J;
+    auto row_max = [&](uint32_t m) {
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if constexpr (kWarps > 1) {
+            if (lane == 0) red[part][warp] = m;
+            asm volatile("bar.sync %0, %1;" ::"r"(part + 1), "n"(kSpan) : "memory");
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) m = max(m, red[part][i]);
+            asm volatile("bar.sync %0, %1;" ::"r"(part + 1), "n"(kSpan) : "memory");  // before the next row's
+        }
+        return m;
+    };
+    for (int64_t row = (int64_t)blockIdx.x * kRows + part; row < p.n_rows; row += (int64_t)gridDim.x * kRows) {
         int64_t g, lo;
         if (!find_group(p, row, g, lo)) continue;
-        const int64_t src = p.rows ? (int64_t)__ldg(p.rows + row) : row;
-        if (src < 0 || src / p.row_div >= p.n_src) continue;
-        const Tin* x = X + (src / p.row_div) * p.ld;
-        float w[16];
-        uint32_t mb = 0;
-        for (int64_t j = tid; j < p.J; j += kTokThreads) {
-            Vec16<Tin>::load(x + 16 * j, w);
-            mb = max(mb, block_max_bits(w));
+        int64_t src = row;
+        if (p.rows) {
+            const int f = __ldg(p.rows + row);
+            src = f < 0 ? -1 : (int64_t)((uint32_t)f / p.row_div);
         }
-        mb = __reduce_max_sync(0xFFFFFFFFu, mb);
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = mb;
-        __syncthreads();
+        if (src < 0 || src >= p.n_src) continue;
+        const Tin* x = X + src * p.ld;
+        Held<Tin> h[kN];
+        uint32_t bb[kN], mb = 0;
+        float gs;
+        bool reload = true;
+        if (p.gamax) {
+            gs = __fdiv_rn(__ldg(p.gamax), 2688.0f);
+        } else {
+            for (int j0 = tid; j0 - tid < J; j0 += kSpan * kN) {
 #pragma unroll
-        for (int i = 0; i < kTokThreads / 32; ++i) mb = max(mb, red[i]);
-        const bool bad_row = mb >= 0x7F800000u;
-        const float gs = __fdiv_rn(p.gamax ? __ldg(p.gamax) : __uint_as_float(mb), 2688.0f);
-        const float nan = __int_as_float(0x7FFFFFFF);
-        if (tid == 0) p.gscale[row] = bad_row ? nan : gs;
-        const int64_t r = row - lo;
-        const int64_t tile = group_tile(lo, g) + r / kTileRows;
-        const int rt = (int)(r % kTileRows);
-        for (int64_t j = tid; j < 4 * p.steps; j += kTokThreads) {
-            uint32_t code = 0;
-            if (j < p.J) {
-                Vec16<Tin>::load(x + 16 * j, w);
-                const uint32_t bb = block_max_bits(w);
-                float s;
-                if (bb >= 0x7F800000u || (bad_row && !p.gamax)) {
-                    code = 0x7F;
-                    s = nan;
-                } else {
-                    code = 1;
-                    if (gs != 0.0f) {
-                        const int c = e4m3_rne_code(__fdiv_rn(__fdiv_rn(__uint_as_float(bb), 6.0f), gs));
-                        code = c < 1 ? 1 : c;
-                    }
-                    s = __fmul_rn(e4m3_value((int)code), gs);
+                for (int i = 0; i < kN; ++i)
+                    if (j0 + i * kSpan < J) h[i].load(x + 16 * (int64_t)(j0 + i * kSpan), p.wide_in);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    bb[i] = j0 + i * kSpan < J ? h[i].max_bits() : 0;
+                    mb = max(mb, bb[i]);
                 }
-                float o[16];
-                uint32_t word[2];
-                quantize_block<kOut, true>(w, s, o, word);
-                reinterpret_cast<uint2*>(p.packed)[row * p.J + j] = make_uint2(word[0], word[1]);
-                if constexpr (kOut) Vec16<Tout>::store(out + (row * p.J + j) * 16, o);
             }
-            p.tiles[scale_offset(tile, rt, j >> 2, p.steps) + (j & 3)] = (uint8_t)code;
+            mb = row_max(mb);
+            gs = __fdiv_rn(__uint_as_float(mb), 2688.0f);
+            reload = J > kSpan * kN;
         }
+        const bool bad_token = mb >= 0x7F800000u;
+        const RowScale rs(gs);
+        const int64_t r = row - lo;
+        uint8_t* tiles = p.tiles + scale_offset(group_tile(lo, g) + r / kTileRows, (int)(r % kTileRows), 0, p.steps);
+        for (int j0 = tid; j0 - tid < 4 * (int)p.steps; j0 += kSpan * kN) {
+            if (reload) {
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (j0 + i * kSpan < J) h[i].load(x + 16 * (int64_t)(j0 + i * kSpan), p.wide_in);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    bb[i] = j0 + i * kSpan < J ? h[i].max_bits() : 0;
+                    mb = max(mb, bb[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int j = j0 + i * kSpan;
+                if (j - lane >= 4 * (int)p.steps) break;  // the same for the warp
+                uint32_t code = 0;
+                if (j < J) {
+                    float s;
+                    code = rs.code(__uint_as_float(bb[i]), s);
+                    if (bb[i] >= 0x7F800000u || bad_token) {
+                        code = 0x7F;
+                        s = rs.nan;
+                    }
+                    float w[16], o[16];
+                    uint32_t word[2];
+                    h[i].floats(w);
+                    quantize_block<kOut, true>(w, s, o, word);
+                    reinterpret_cast<uint2*>(p.packed)[row * J + j] = make_uint2(word[0], word[1]);
+                    if constexpr (kOut) store16(out + (row * J + j) * 16, o, p.wide_out);
+                }
+                // the four codes of a step, one word of the tile
+                uint32_t v = code << (8 * (j & 3));
+                v |= __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                v |= __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+                if ((j & 3) == 0 && j < 4 * (int)p.steps)
+                    *reinterpret_cast<uint32_t*>(tiles + (int64_t)(j >> 2) * kTileBytes) = v;
+            }
+        }
+        if (p.gamax) mb = row_max(mb);
+        if (tid == 0) p.gscale[row] = mb >= 0x7F800000u ? rs.nan : gs;
     }
 }
 
@@ -135,23 +287,44 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restr
     }
 }
 
-template <typename Tin, bool kOut>
-lh_status launch_tokens(const void* X, const TokenArgs& p, void* out, lh_dtype out_dtype, int sms, cudaStream_t st) {
-    const int64_t cap = (int64_t)sms * 8;
+template <typename Tin, typename Tout, bool kOut, int kWarps>
+lh_status launch_tokens_w(const void* X, const TokenArgs& p, void* out, int sms, cudaStream_t st) {
+    constexpr int kRows = 8 / kWarps;
+    const int64_t need = (p.n_rows + kRows - 1) / kRows, cap = (int64_t)sms * 16;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.n_rows < cap ? p.n_rows : cap));
-    cfg.blockDim = dim3(kTokThreads);
+    cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (out_dtype == LH_BF16)
-        return cuda_status(cudaLaunchKernelEx(&cfg, tokens_kernel<Tin, uint16_t, kOut>, (const Tin*)X, p, (uint16_t*)out),
-                           "tokens_kernel launch");
-    return cuda_status(cudaLaunchKernelEx(&cfg, tokens_kernel<Tin, float, kOut>, (const Tin*)X, p, (float*)out),
+    return cuda_status(cudaLaunchKernelEx(&cfg, tokens_kernel<Tin, Tout, kOut, kWarps>, (const Tin*)X, p, (Tout*)out),
                        "tokens_kernel launch");
+}
+
+template <typename Tin, typename Tout, bool kOut>
+lh_status launch_tokens_o(const void* X, const TokenArgs& p, void* out, int sms, cudaStream_t st) {
+    // enough warps to hold the row (its own scale), and while the rows leave SMs idle
+    // enough to load it in one go
+    int warps = 1;
+    while (warps < 8 && ((!p.gamax && p.J > 32 * kHeld<Tin> * warps) ||
+                         (p.J > 32 * warps && p.n_rows * warps * 2 <= 16 * (int64_t)sms)))
+        warps *= 2;
+    switch (warps) {
+        case 1: return launch_tokens_w<Tin, Tout, kOut, 1>(X, p, out, sms, st);
+        case 2: return launch_tokens_w<Tin, Tout, kOut, 2>(X, p, out, sms, st);
+        case 4: return launch_tokens_w<Tin, Tout, kOut, 4>(X, p, out, sms, st);
+        default: return launch_tokens_w<Tin, Tout, kOut, 8>(X, p, out, sms, st);
+    }
+}
+
+template <typename Tin>
+lh_status launch_tokens(const void* X, const TokenArgs& p, void* out, lh_dtype out_dtype, int sms, cudaStream_t st) {
+    if (!out) return launch_tokens_o<Tin, float, false>(X, p, nullptr, sms, st);
+    if (out_dtype == LH_BF16) return launch_tokens_o<Tin, uint16_t, true>(X, p, out, sms, st);
+    return launch_tokens_o<Tin, float, true>(X, p, out, sms, st);
 }
 
 }  // namespace
@@ -202,6 +375,7 @@ extern "C" lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t
     if (n_src < 0 || n_rows < 0 || c_in < 0 || n_groups < 1)
         return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
     if (row_div < 1) return fail(LH_ERR_INVALID_ARG, "row_div must be >= 1");
+    if (row_div > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "row_div must be below 2^31");
     if (!rows && (row_div != 1 || n_rows > n_src))
         return fail(LH_ERR_INVALID_ARG, "without rows, row_div must be 1 and n_rows at most n_src");
     if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
@@ -211,20 +385,20 @@ extern "C" lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t
         return fail(LH_ERR_ALIGNMENT, "X must be 16-byte aligned with 16-byte aligned rows");
     if (!aligned16(packed) || !aligned16(scale_tiles) || !aligned16(X_out))
         return fail(LH_ERR_ALIGNMENT, "packed, scale_tiles and X_out must be 16-byte aligned");
+    if (c_in > INT_MAX - 64) return fail(LH_ERR_UNSUPPORTED, "c_in must be below 2^31 - 64");
     if (X == X_out || X == (const void*)packed || X == (const void*)scale_tiles || packed == scale_tiles)
         return fail(LH_ERR_INVALID_ARG, "outputs must not alias X or one another");
     if (n_rows == 0 || c_in == 0 || n_src == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     TokenArgs p;
-    p.n_src = n_src; p.ld = ld_x; p.row_div = row_div; p.n_rows = n_rows;
+    p.n_src = n_src; p.ld = ld_x; p.row_div = (uint32_t)row_div; p.n_rows = n_rows;
     p.G = n_groups; p.J = c_in / 16; p.steps = scale_steps(c_in);
     p.rows = (const int*)rows; p.offsets = offsets; p.gamax = global_amax;
+    p.wide_in = (reinterpret_cast<uintptr_t>(X) & 31) == 0 && (ld_x * elem_bytes(x_dtype)) % 32 == 0;
+    p.wide_out = (reinterpret_cast<uintptr_t>(X_out) & 31) == 0;
     p.packed = packed; p.tiles = scale_tiles; p.gscale = token_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (x_dtype == LH_BF16)
-        return X_out ? launch_tokens<uint16_t, true>(X, p, X_out, out_dtype, sms, st)
-                     : launch_tokens<uint16_t, false>(X, p, nullptr, LH_F32, sms, st);
-    return X_out ? launch_tokens<float, true>(X, p, X_out, out_dtype, sms, st)
-                 : launch_tokens<float, false>(X, p, nullptr, LH_F32, sms, st);
+    if (x_dtype == LH_BF16) return launch_tokens<uint16_t>(X, p, X_out, out_dtype, sms, st);
+    return launch_tokens<float>(X, p, X_out, out_dtype, sms, st);
 }
