@@ -21,6 +21,10 @@
 #include "scale_tiles.cuh"
 #include "tcgen05.cuh"
 
+#ifndef PAIRT
+#define PAIRT 256
+#endif
+
 namespace lh {
 namespace {
 
@@ -138,6 +142,94 @@ __device__ __forceinline__ void give_up(volatile int* flag) {
 
 __device__ __forceinline__ void store_out(float* y, float v) { *y = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+
+// A warp's part of a finished tile: 32 channels (its TMEM lanes) x up to 128 tokens, into
+// registers and from there to Y. Row-major Y wants a token's channels side by side. In f32
+// a lane per channel does that (128 bytes a store). In bf16 the values are taken in the
+// layout of mma fragments and turned by stmatrix through 32 rows of shared memory (80
+// bytes apart, which keeps both ways free of bank conflicts), so that a lane stores 8
+// channels at once.
+constexpr int kTurnRow = 80, kTurnBytes = 32 * kTurnRow;
+
+template <typename Tout>
+struct Part;
+
+template <>
+struct Part<float> {
+    uint32_t r[4][32];
+    __device__ void take(uint32_t src, int n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (32 * j < n) tmem_ld32(src + 32 * j, r[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
+    }
+    // gx[j]: this lane's token 32 j + lane; y: the first token's row; ch0: the warp's first channel
+    __device__ void put(const float (&gx)[4], int n, float* y, int64_t ld, int64_t ch0, int64_t c_out, uint8_t*) {
+        const int64_t ch = ch0 + (threadIdx.x & 31);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (32 * j >= n) break;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float s = __shfl_sync(0xFFFFFFFFu, gx[j], i);
+                if (32 * j + i < n && ch < c_out) y[(int64_t)(32 * j + i) * ld + ch] = __uint_as_float(r[j][i]) * s;
+            }
+        }
+    }
+};
+
+template <>
+struct Part<__nv_bfloat16> {
+    uint32_t r[4][32];  // [2 (token / 64) + lane / 16]
+    __device__ void take(uint32_t src, int n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (64 * (j >> 1) < n) tmem_ld16x64(src + 64 * (j >> 1) + ((uint32_t)(16 * (j & 1)) << 16), r[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
+    }
+    __device__ static uint32_t pack(uint32_t lo, float sl, uint32_t hi, float sh) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo) * sl, __uint_as_float(hi) * sh);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ void put(const float (&gx)[4], int n, __nv_bfloat16* y, int64_t ld, int64_t ch0, int64_t c_out,
+                        uint8_t* turn) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t dst = smem_u32(turn) + (lane & 7) * kTurnRow + (lane >> 3) * 16;
+        const int64_t ch = ch0 + 8 * (lane & 3);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // 32 tokens
+            if (32 * c >= n) break;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // 8 tokens
+                const float s0 = __shfl_sync(0xFFFFFFFFu, gx[c], 8 * j + 2 * (lane & 3));
+                const float s1 = __shfl_sync(0xFFFFFFFFu, gx[c], 8 * j + 2 * (lane & 3) + 1);
+                const uint32_t* a = r[2 * (c >> 1)] + 16 * (c & 1) + 4 * j;
+                const uint32_t* b = r[2 * (c >> 1) + 1] + 16 * (c & 1) + 4 * j;
+                stmatrix4_trans(dst + 8 * j * kTurnRow, pack(a[0], s0, a[1], s1), pack(a[2], s0, a[3], s1),
+                                pack(b[0], s0, b[1], s1), pack(b[2], s0, b[3], s1));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = 8 * q + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4*>(turn + row * kTurnRow + (lane & 3) * 16);
+                if (32 * c + row >= n) continue;
+                __nv_bfloat16* to = y + (int64_t)(32 * c + row) * ld + ch;
+                if (ch + 8 <= c_out) {
+                    *reinterpret_cast<uint4*>(to) = v;
+                } else {
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (ch + i < c_out) to[i] = __ushort_as_bfloat16((uint16_t)(u[i >> 1] >> (16 * (i & 1))));
+                }
+            }
+        }
+    }
+};
 
 template <int T, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
@@ -305,30 +397,37 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // the scales 96, which leaves no room for a second one: eight epilogue warps take a
 // whole accumulator into registers and free it before they scale and store.
 
-constexpr int kPairT = 256;
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
-constexpr int kPairStages = 5;
-constexpr int kPairA = kM * kRowBytes, kPairB = kPairT / 2 * kRowBytes;
-constexpr int kPairSa = 4 * kTileBytes, kPairSb = 2 * 4 * kTileBytes;
-constexpr int kPairStageBytes = kPairA + kPairB + kPairSa + kPairSb;
-constexpr int kPairScaleCol = kPairT, kPairSetCols = 16 + 32;
+constexpr int kPairRows = 256;     // rows per group from which the pairs are taken
 
-constexpr int kPairRows = 256;  // rows per group from which the pairs are taken
+template <int T>
+struct Pair {
+    static constexpr int kAcc = T > 192 ? 1 : 2;  // accumulators in TMEM
+    static constexpr int kA = kM * kRowBytes, kB = T / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = 2 * 4 * kTileBytes;
+    static constexpr int kStageBytes = kA + kB + kSa + kSb;
+    static constexpr int kStages = T > 192 ? 5 : 6;
+    static constexpr int kScaleCol = kAcc * T, kSetCols = 16 + 32;
+    static_assert(kScaleCol + 2 * kSetCols <= 512, "TMEM columns");
+    static_assert(T % 32 == 0 && T <= 256, "scales of a tile start on a lane 0 and span two tiles");
+};
 
+template <int T>
 struct PairControl {
-    uint64_t full[kPairStages], empty[kPairStages], tfull, tempty, drain;
+    uint64_t full[Pair<T>::kStages], empty[Pair<T>::kStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
 };
 
-template <typename Tout>
+template <int T, typename Tout>
 __global__ void __launch_bounds__(kPairThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                         const ProdArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    PairControl& C = *reinterpret_cast<PairControl*>(base_p + kPairStages * kPairStageBytes);
+    using S = Pair<T>;
+    uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
+    PairControl<T>& C = *reinterpret_cast<PairControl<T>*>(turn_p + 8 * kTurnBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,12 +435,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&C.full[s]), 1);
             mbar_init(smem_u32(&C.empty[s]), 1);
         }
-        mbar_init(smem_u32(&C.tfull), 1);
-        mbar_init(smem_u32(&C.tempty), 16);  // the epilogue warps of both CTAs
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&C.tfull[a]), 1);
+            mbar_init(smem_u32(&C.tempty[a]), 16);  // the epilogue warps of both CTAs
+        }
         mbar_init(smem_u32(&C.drain), 1);
         C.abort_flag = 0;
         mbar_init_fence();
@@ -354,7 +455,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = C.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk<kPairT> walk;
+    Walk<T> walk;
     Tile t;
     if (warp == 0) {
         int stage = 0;
@@ -372,8 +473,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = cluster_addr(smem_u32(&C.full[stage]), 0);
-                    const uint32_t a = ring + stage * kPairStageBytes, b = a + kPairA, sa = b + kPairB, sb = sa + kPairSa;
-                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), 2 * kPairStageBytes);
+                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
+                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), 2 * S::kStageBytes);
                     tma_load_2d_pair(a, &wmap, ks * kRowBytes, wrow, bar);
                     tma_load_2d_pair(b, &xmap, ks * kRowBytes, xrow, bar);
                     // past the last step or tile these bring other scales, or zeros, that no product uses
@@ -383,28 +484,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 __syncwarp();
                 ++issued;
-                if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
         }
         if (!ok) {  // the loads in flight land before the CTAs end (both report to the first one's barriers)
             give_up(abort_flag);
-            const int n = rank == 0 ? (issued < kPairStages ? (int)issued : kPairStages) : 0;
+            const int n = rank == 0 ? (issued < S::kStages ? (int)issued : S::kStages) : 0;
             for (int i = 0; i < n; ++i) {
-                if (--stage < 0) { stage = kPairStages - 1; phase ^= 1; }
+                if (--stage < 0) { stage = S::kStages - 1; phase ^= 1; }
                 int none = 0;
                 warp_wait(smem_u32(&C.full[stage]), phase, &none);
             }
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0;
+            int stage = 0, acc = 0;
             uint32_t phase = 0, aphase = 0, set = 0;
             bool ok = true;
             for (int u = first; ok && walk.find(p, u, t); u += step) {
-                ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
+                ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
                 if (!ok) break;
                 fence_after();
                 const uint32_t n16 = (t.rows + 15) & ~15;
+                const uint32_t d = tmem + acc * T, sub_col = (t.sub % kTileRows) / 32;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
                 for (int ks = 0; ks < p.stages_k; ++ks) {
                     ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
@@ -412,25 +514,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     fence_after();
                     if (elect_one()) {
                         const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                        const uint32_t a = ring + stage * kPairStageBytes, b = a + kPairA, sa = b + kPairB,
-                                       sb = sa + kPairSa;
-                        const uint32_t ca = tmem + kPairScaleCol + set * kPairSetCols, cb = ca + 16;
+                        const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB,
+                                       sb = sa + S::kSa;
+                        const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                        // step by step: the copies of a step run beside the products of the one before
                         for (int k = 0; k < nk; ++k) {
                             tmem_cp_scales_pair(ca + 4 * k, desc_scales(sa + k * kTileBytes));
                             tmem_cp_scales_pair(cb + 8 * k, desc_scales(sb + k * kTileBytes));
                             tmem_cp_scales_pair(cb + 8 * k + 4, desc_scales(sb + (4 + k) * kTileBytes));
+                            mma_nvfp4_pair(d, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
+                                           cb + 8 * k + sub_col, (ks | k) ? 1u : 0u);
                         }
-                        for (int k = 0; k < nk; ++k)
-                            mma_nvfp4_pair(tmem, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
-                                           cb + 8 * k, (ks | k) ? 1u : 0u);
                         mma_commit_pair(smem_u32(&C.empty[stage]));
-                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
+                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull[acc]));
                     }
                     __syncwarp();
                     set ^= 1;
-                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                    if (++stage == S::kStages) { stage = 0; phase ^= 1; }
                 }
-                aphase ^= 1;
+                if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
             }
             if (!ok) {  // the products in flight end before the CTAs do
                 give_up(abort_flag);
@@ -443,41 +545,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else {
         const int q = warp & 3;           // the TMEM lanes that this warp can read
         const int h = (warp - 2) >> 2;    // its half of the tokens
-        const uint32_t tempty = cluster_addr(smem_u32(&C.tempty), 0);
+        uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
+        int acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
         for (int u = first; ok && walk.find(p, u, t); u += step) {
-            const int64_t ch = (int64_t)t.mt * 2 * kM + rank * kM + q * 32 + lane;
+            const int64_t ch0 = (int64_t)t.mt * 2 * kM + rank * kM + q * 32;
             const float gw = __ldg(p.wg + t.g);
-            const int c0 = h * 128, n = t.rows - c0;  // tokens of this warp, if above 0 (128 at most)
+            const int c0 = h * (T / 2);
+            const int n = t.rows - c0 < T / 2 ? t.rows - c0 : T / 2;  // tokens of this warp, if above 0
             float gx[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 gx[j] = 32 * j + lane < n ? gw * __ldg(p.xg + t.row0 + c0 + 32 * j + lane) : 0.0f;
-            ok = warp_wait(smem_u32(&C.tfull), aphase, abort_flag);
+            ok = warp_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
             if (!ok) break;
             fence_after();
-            uint32_t r[4][32];
-            const uint32_t src = tmem + ((uint32_t)(q * 32) << 16) + c0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (32 * j < n) tmem_ld32(src + 32 * j, r[j]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
+            Part<Tout> part;
+            part.take(tmem + ((uint32_t)(q * 32) << 16) + acc * T + c0, n);
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty);
-            aphase ^= 1;
-            Tout* y = static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y + ch;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float s = __shfl_sync(0xFFFFFFFFu, gx[j], i);
-                    if (32 * j + i < n && ch < p.c_out)
-                        store_out(y + (int64_t)(32 * j + i) * p.ld_y, __uint_as_float(r[j][i]) * s);
-                }
-            }
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty[acc]), 0));
+            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+            part.put(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn);
         }
         if (!ok) give_up(abort_flag);
     }
@@ -553,22 +643,22 @@ bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Tout>
+template <int T, typename Tout>
 lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                       ProdArgs p, int sms, cudaStream_t st) {
     p.mtiles = (p.mtiles128 + 1) / 2;
-    const int64_t tiles = (p.offsets ? p.n_rows / kPairT + p.G : (p.n_rows + kPairT - 1) / kPairT) * p.mtiles;
+    const int64_t tiles = (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "too many tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kPairT / 2) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T / 2) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    constexpr size_t smem = (size_t)kPairStages * kPairStageBytes + 1024 + sizeof(PairControl);
+    constexpr size_t smem = (size_t)Pair<T>::kStages * Pair<T>::kStageBytes + 8 * kTurnBytes + 1024 + sizeof(PairControl<T>);
     static_assert(smem <= 227 * 1024, "shared memory");
-    auto kernel = product_pair_kernel<Tout>;
+    auto kernel = product_pair_kernel<T, Tout>;
     lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                               "product_pair_kernel shared memory");
     if (s != LH_OK) return s;
@@ -638,8 +728,8 @@ extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_s
     p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (n_rows >= kPairRows * n_groups) {
-        if (out_dtype == LH_BF16) return launch_pair<__nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
-        return launch_pair<float>(encode, X_packed, W_packed, c_in, p, sms, st);
+        if (out_dtype == LH_BF16) return launch_pair<PAIRT, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
+        return launch_pair<PAIRT, float>(encode, X_packed, W_packed, c_in, p, sms, st);
     }
     if (out_dtype == LH_BF16) return launch_product<128, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
     return launch_product<128, float>(encode, X_packed, W_packed, c_in, p, sms, st);
