@@ -21,10 +21,6 @@
 #include "scale_tiles.cuh"
 #include "tcgen05.cuh"
 
-#ifndef PAIRT
-#define PAIRT 256
-#endif
-
 namespace lh {
 namespace {
 
@@ -50,25 +46,25 @@ struct ProdArgs {
     const float* xg;         // [n_rows]
     const float* wg;         // [G]
     void* Y;
+    bool early;              // the kernel before leaves weights, scales and offsets alone: no need to wait for those
 };
 
-template <int T>
+constexpr int kT = 128;            // tokens of a tile: one scale tile
+constexpr int kBox = 32;           // tokens of one TMA copy: a tile brings the rows it has, rounded up to these
+
 struct Shape {
-    static constexpr int kScaleTiles = (T + kTileRows - 1) / kTileRows;  // token scale tiles per step
-    static constexpr int kA = kM * kRowBytes, kB = T * kRowBytes;
-    static constexpr int kSa = 4 * kTileBytes, kSb = 4 * kTileBytes * kScaleTiles;
+    static constexpr int kA = kM * kRowBytes, kB = kT * kRowBytes, kSa = 4 * kTileBytes, kSb = 4 * kTileBytes;
     static constexpr int kStageBytes = kA + kB + kSa + kSb;
-    static constexpr int kStages = (220 * 1024) / kStageBytes < 8 ? (220 * 1024) / kStageBytes : 8;
-    static constexpr int kAcc = T > 128 ? 1 : 2;                         // accumulators in TMEM
-    static constexpr int kScaleCol = kAcc * T < 32 ? 32 : kAcc * T;      // first TMEM column of the scales
-    static constexpr int kSetCols = 16 + 16 * kScaleTiles;               // scales of one stage
-    static constexpr int kTmemCols = 512;
+    static constexpr int kStages = 6;
+    // TMEM: two accumulators, then the scales of two stages (addresses of scales are
+    // multiples of 4 columns, so a tile starts with a scale tile)
+    static constexpr int kScaleCol = 2 * kT, kSetCols = 32, kTmemCols = 512;
     static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "TMEM columns");
+    static_assert(kStages * kStageBytes >= kT * kM * 4, "split: the partial sums reuse the ring");
 };
 
-template <int T>
 struct Control {
-    uint64_t full[Shape<T>::kStages], empty[Shape<T>::kStages], tfull[2], tempty[2], drain;
+    uint64_t full[Shape::kStages], empty[Shape::kStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
 };
@@ -146,10 +142,10 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __fl
 // A warp's part of a finished tile: 32 channels (its TMEM lanes) x up to 128 tokens, into
 // registers and from there to Y. Row-major Y wants a token's channels side by side. In f32
 // a lane per channel does that (128 bytes a store). In bf16 the values are taken in the
-// layout of mma fragments and turned by stmatrix through 32 rows of shared memory (80
-// bytes apart, which keeps both ways free of bank conflicts), so that a lane stores 8
-// channels at once.
-constexpr int kTurnRow = 80, kTurnBytes = 32 * kTurnRow;
+// layout of mma fragments and turned by stmatrix through 32 rows of 64 bytes of shared
+// memory (their 16-byte pieces swapped by the row's number, which keeps both ways free of
+// bank conflicts), so that a lane stores 8 channels at once.
+constexpr int kTurnRow = 64, kTurnBytes = 32 * kTurnRow;
 
 template <typename Tout>
 struct Part;
@@ -196,7 +192,7 @@ struct Part<__nv_bfloat16> {
     __device__ void put(const float (&gx)[4], int n, __nv_bfloat16* y, int64_t ld, int64_t ch0, int64_t c_out,
                         uint8_t* turn) {
         const int lane = threadIdx.x & 31;
-        const uint32_t dst = smem_u32(turn) + (lane & 7) * kTurnRow + (lane >> 3) * 16;
+        const uint32_t dst = smem_u32(turn) + (lane & 7) * kTurnRow + (((lane >> 3) ^ (lane >> 1)) & 3) * 16;
         const int64_t ch = ch0 + 8 * (lane & 3);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 32 tokens
@@ -215,7 +211,7 @@ struct Part<__nv_bfloat16> {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int row = 8 * q + (lane >> 2);
-                const uint4 v = *reinterpret_cast<const uint4*>(turn + row * kTurnRow + (lane & 3) * 16);
+                const uint4 v = *reinterpret_cast<const uint4*>(turn + row * kTurnRow + (((lane & 3) ^ (row >> 1)) & 3) * 16);
                 if (32 * c + row >= n) continue;
                 __nv_bfloat16* to = y + (int64_t)(32 * c + row) * ld + ch;
                 if (ch + 8 <= c_out) {
@@ -231,17 +227,24 @@ struct Part<__nv_bfloat16> {
     }
 };
 
-template <int T, typename Tout>
+// kSplit: a cluster of CTAs works on one tile, each on a part of c_in; the partial sums
+// meet in distributed shared memory, each CTA adding up those of 128 / cluster tokens in the
+// order of the parts (the same sums every time). Without it a CTA walks over whole tiles.
+template <bool kSplit, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
                                                               const ProdArgs p) {
-    using S = Shape<T>;
+    using S = Shape;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Control<T>& C = *reinterpret_cast<Control<T>*>(base_p + S::kStages * S::kStageBytes);
+    uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
+    Control& C = *reinterpret_cast<Control*>(turn_p + 4 * kTurnBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = kSplit ? (int)cluster_size() : 1, rank = kSplit ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / parts, step = gridDim.x / parts;
+    const int ks0 = p.stages_k * rank / parts, ks1 = p.stages_k * (rank + 1) / parts;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -262,35 +265,46 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     fence_after();
     const uint32_t tmem = C.tmem;
     // everything above overlaps the kernel before
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk<T> walk;
+    Walk<kT> walk;
     Tile t;
     if (warp == 0) {
-        int stage = 0;
+        int stage = 0, ahead = 0;  // ahead: stages whose weights are on their way
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
+        for (int u = first; ok && walk.find(p, u, t); u += step) {
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
             const uint8_t* wsrc = p.ws + (t.g * p.mtiles + t.mt) * (int64_t)p.steps * kTileBytes;
-            const int64_t xt = group_tile(t.lo, t.g) + t.sub / kTileRows;
-            const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
-            for (int ks = 0; ks < p.stages_k; ++ks) {
+            const uint8_t* xsrc = p.xs + (group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps * (int64_t)kTileBytes;
+            const int boxes = (t.rows + kBox - 1) / kBox;
+            auto scale_bytes = [&](int ks) { return (p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4) * kTileBytes; };
+            auto weights = [&](int s, int ks) {
+                const uint32_t bar = smem_u32(&C.full[s]), a = ring + s * S::kStageBytes;
+                mbar_expect_tx(bar, S::kA + boxes * kBox * kRowBytes + 2 * scale_bytes(ks));
+                tma_load_2d(a, &wmap, ks * kRowBytes, wrow, bar);
+                bulk_load(a + S::kA + S::kB, wsrc + (int64_t)ks * 4 * kTileBytes, scale_bytes(ks), bar);
+            };
+            if (p.early && u == first) {
+                ahead = ks1 - ks0 < S::kStages ? ks1 - ks0 : S::kStages;
+                if (elect_one())
+                    for (int i = 0; i < ahead; ++i) weights(i, ks0 + i);
+                __syncwarp();
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            }
+            for (int ks = ks0; ks < ks1; ++ks) {
                 ok = warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
                 if (!ok) break;
-                const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
                 if (elect_one()) {
-                    const uint32_t bar = smem_u32(&C.full[stage]);
-                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
-                    mbar_expect_tx(bar, S::kA + S::kB + nk * kTileBytes * (1 + xtiles));
-                    tma_load_2d(a, &wmap, ks * kRowBytes, wrow, bar);
-                    tma_load_2d(b, &xmap, ks * kRowBytes, (int)t.row0, bar);
-                    bulk_load(sa, wsrc + (int64_t)ks * 4 * kTileBytes, nk * kTileBytes, bar);
-                    for (int i = 0; i < xtiles; ++i)
-                        bulk_load(sb + i * 4 * kTileBytes,
-                                  p.xs + ((xt + i) * p.steps + ks * 4) * (int64_t)kTileBytes, nk * kTileBytes, bar);
+                    const uint32_t bar = smem_u32(&C.full[stage]), b = ring + stage * S::kStageBytes + S::kA;
+                    if (ahead == 0) weights(stage, ks);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(b + i * kBox * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * kBox, bar);
+                    bulk_load(b + S::kB + S::kSa, xsrc + (int64_t)ks * 4 * kTileBytes, scale_bytes(ks), bar);
                 }
+                __syncwarp();
+                if (ahead > 0) --ahead;
                 ++issued;
                 if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
@@ -308,17 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int stage = 0, acc = 0;
         uint32_t phase = 0, aphase = 0, set = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
+        for (int u = first; ok && walk.find(p, u, t); u += step) {
             ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
             if (!ok) break;
             fence_after();
             const uint32_t n16 = (t.rows + 15) & ~15;
             // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
             const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
-            const uint32_t d = tmem + acc * T;
-            const uint32_t sub_col = (t.sub % kTileRows) / 32;
-            const int xtiles = (t.sub % kTileRows + t.rows + kTileRows - 1) / kTileRows;
-            for (int ks = 0; ks < p.stages_k; ++ks) {
+            const uint32_t d = tmem + acc * kT;
+            for (int ks = ks0; ks < ks1; ++ks) {
                 ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
                 if (!ok) break;
                 fence_after();
@@ -326,23 +338,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
                     const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
                     const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
-                    for (int k = 0; k < nk; ++k) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= nk) break;
+                        tmem_cp_scales(cb + 4 * k, desc_scales(sb + k * kTileBytes));
                         tmem_cp_scales(ca + 4 * k, desc_scales(sa + k * kTileBytes));
-                        for (int i = 0; i < xtiles; ++i)
-                            tmem_cp_scales(cb + 4 * (k * S::kScaleTiles + i),
-                                           desc_scales(sb + (i * 4 + k) * kTileBytes));
-                    }
-                    for (int k = 0; k < nk; ++k)
                         mma_nvfp4(d, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
-                                  cb + 4 * k * S::kScaleTiles + sub_col, (ks | k) ? 1u : 0u);
+                                  cb + 4 * k, (ks > ks0 || k > 0) ? 1u : 0u);
+                    }
                     mma_commit(smem_u32(&C.empty[stage]));
-                    if (ks == p.stages_k - 1) mma_commit(smem_u32(&C.tfull[acc]));
+                    if (ks == ks1 - 1) mma_commit(smem_u32(&C.tfull[acc]));
                 }
                 __syncwarp();
                 set ^= 1;
                 if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
-            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+            if (++acc == 2) { acc = 0; aphase ^= 1; }
         }
         if (!ok) {  // the products in flight end before the CTA does
             give_up(abort_flag);
@@ -351,36 +362,70 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int none = 0;
             warp_wait(smem_u32(&C.drain), 0, &none);
         }
-    } else {
+    } else if (!kSplit) {
+        if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         const int q = warp & 3;  // the TMEM lanes that this warp can read
+        uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
         int acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && walk.find(p, u, t); u += gridDim.x) {
-            const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
+        for (int u = first; ok && walk.find(p, u, t); u += step) {
             const float gw = __ldg(p.wg + t.g);
+            float gx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                gx[j] = 32 * j + lane < t.rows ? gw * __ldg(p.xg + t.row0 + 32 * j + lane) : 0.0f;
             ok = warp_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
             if (!ok) break;
             fence_after();
-            Tout* y = static_cast<Tout*>(p.Y) + t.row0 * p.ld_y + ch;
-            for (int c = 0; c < t.rows; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * T + c, r);
-                tmem_wait32(r);
-                if (ch < p.c_out) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < t.rows)
-                            store_out(y + (int64_t)(c + i) * p.ld_y,
-                                      __uint_as_float(r[i]) * (gw * __ldg(p.xg + t.row0 + c + i)));
-                }
-            }
+            Part<Tout> part;
+            part.take(tmem + ((uint32_t)(q * 32) << 16) + acc * kT, t.rows);
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&C.tempty[acc]));
-            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+            if (++acc == 2) { acc = 0; aphase ^= 1; }
+            part.put(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y, (int64_t)t.mt * kM + q * 32, p.c_out,
+                     turn);
         }
         if (!ok) give_up(abort_flag);
+    } else {
+        if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (walk.find(p, first, t) && !warp_wait(smem_u32(&C.tfull[0]), 0, abort_flag)) give_up(abort_flag);
+    }
+    if constexpr (kSplit) {
+        // one tile: every CTA of the cluster is done with its ring, which now takes the
+        // sums, [part][its tokens][channel]
+        __syncwarp();
+        cluster_sync();
+        const int per = kT / parts, q = warp & 3;
+        float* sums = reinterpret_cast<float*>(base_p);
+        if (warp >= 2) {
+            fence_after();
+            for (int c = 0; c < t.rows; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, r);
+                tmem_wait32(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (c + i >= t.rows) break;
+                    const int to = (c + i) / per;
+                    const uint32_t at = smem_u32(sums + (rank * per + (c + i - to * per)) * kM + q * 32 + lane);
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr(at, to)), "r"(r[i]) : "memory");
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2) {
+            const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
+            const float gw = __ldg(p.wg + t.g);
+            for (int i = 0; i < per && rank * per + i < t.rows; ++i) {
+                const int64_t row = t.row0 + rank * per + i;
+                float v = 0.0f;
+                for (int s = 0; s < parts; ++s) v += sums[(s * per + i) * kM + q * 32 + lane];
+                if (ch < p.c_out) store_out(static_cast<Tout*>(p.Y) + row * p.ld_y + ch, v * (gw * __ldg(p.xg + row)));
+            }
+        }
     }
     fence_before();
     __syncthreads();
@@ -400,34 +445,32 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairRows = 256;     // rows per group from which the pairs are taken
 
-template <int T>
+constexpr int kPairT = 256;        // tokens of a pair's tile: two scale tiles
+
 struct Pair {
-    static constexpr int kAcc = T > 192 ? 1 : 2;  // accumulators in TMEM
-    static constexpr int kA = kM * kRowBytes, kB = T / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = 2 * 4 * kTileBytes;
+    static constexpr int kA = kM * kRowBytes, kB = kPairT / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = 2 * 4 * kTileBytes;
     static constexpr int kStageBytes = kA + kB + kSa + kSb;
-    static constexpr int kStages = T > 192 ? 5 : 6;
-    static constexpr int kScaleCol = kAcc * T, kSetCols = 16 + 32;
+    static constexpr int kStages = 5;
+    static constexpr int kScaleCol = kPairT, kSetCols = 16 + 32;
     static_assert(kScaleCol + 2 * kSetCols <= 512, "TMEM columns");
-    static_assert(T % 32 == 0 && T <= 256, "scales of a tile start on a lane 0 and span two tiles");
 };
 
-template <int T>
 struct PairControl {
-    uint64_t full[Pair<T>::kStages], empty[Pair<T>::kStages], tfull[2], tempty[2], drain;
+    uint64_t full[Pair::kStages], empty[Pair::kStages], tfull, tempty, drain;
     uint32_t tmem;
     int abort_flag;
 };
 
-template <int T, typename Tout>
+template <typename Tout>
 __global__ void __launch_bounds__(kPairThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                         const ProdArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    using S = Pair<T>;
+    using S = Pair;
     uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
-    PairControl<T>& C = *reinterpret_cast<PairControl<T>*>(turn_p + 8 * kTurnBytes);
+    PairControl& C = *reinterpret_cast<PairControl*>(turn_p + 8 * kTurnBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -439,10 +482,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_u32(&C.full[s]), 1);
             mbar_init(smem_u32(&C.empty[s]), 1);
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(smem_u32(&C.tfull[a]), 1);
-            mbar_init(smem_u32(&C.tempty[a]), 16);  // the epilogue warps of both CTAs
-        }
+        mbar_init(smem_u32(&C.tfull), 1);
+        mbar_init(smem_u32(&C.tempty), 16);  // the epilogue warps of both CTAs
         mbar_init(smem_u32(&C.drain), 1);
         C.abort_flag = 0;
         mbar_init_fence();
@@ -455,7 +496,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = C.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk<T> walk;
+    Walk<kPairT> walk;
     Tile t;
     if (warp == 0) {
         int stage = 0;
@@ -498,15 +539,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0, acc = 0;
+            int stage = 0;
             uint32_t phase = 0, aphase = 0, set = 0;
             bool ok = true;
             for (int u = first; ok && walk.find(p, u, t); u += step) {
-                ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
+                ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
                 if (!ok) break;
                 fence_after();
                 const uint32_t n16 = (t.rows + 15) & ~15;
-                const uint32_t d = tmem + acc * T, sub_col = (t.sub % kTileRows) / 32;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
                 for (int ks = 0; ks < p.stages_k; ++ks) {
                     ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
@@ -518,21 +558,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                        sb = sa + S::kSa;
                         const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
                         // step by step: the copies of a step run beside the products of the one before
-                        for (int k = 0; k < nk; ++k) {
-                            tmem_cp_scales_pair(ca + 4 * k, desc_scales(sa + k * kTileBytes));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k >= nk) break;
                             tmem_cp_scales_pair(cb + 8 * k, desc_scales(sb + k * kTileBytes));
                             tmem_cp_scales_pair(cb + 8 * k + 4, desc_scales(sb + (4 + k) * kTileBytes));
-                            mma_nvfp4_pair(d, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
-                                           cb + 8 * k + sub_col, (ks | k) ? 1u : 0u);
+                            tmem_cp_scales_pair(ca + 4 * k, desc_scales(sa + k * kTileBytes));
+                            mma_nvfp4_pair(tmem, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
+                                           cb + 8 * k, (ks | k) ? 1u : 0u);
                         }
                         mma_commit_pair(smem_u32(&C.empty[stage]));
-                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull[acc]));
+                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
                     }
                     __syncwarp();
                     set ^= 1;
                     if (++stage == S::kStages) { stage = 0; phase ^= 1; }
                 }
-                if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+                aphase ^= 1;
             }
             if (!ok) {  // the products in flight end before the CTAs do
                 give_up(abort_flag);
@@ -546,27 +588,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int q = warp & 3;           // the TMEM lanes that this warp can read
         const int h = (warp - 2) >> 2;    // its half of the tokens
         uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
-        int acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
         for (int u = first; ok && walk.find(p, u, t); u += step) {
             const int64_t ch0 = (int64_t)t.mt * 2 * kM + rank * kM + q * 32;
             const float gw = __ldg(p.wg + t.g);
-            const int c0 = h * (T / 2);
-            const int n = t.rows - c0 < T / 2 ? t.rows - c0 : T / 2;  // tokens of this warp, if above 0
+            const int c0 = h * (kPairT / 2);
+            const int n = t.rows - c0 < kPairT / 2 ? t.rows - c0 : kPairT / 2;  // tokens of this warp, if above 0
             float gx[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 gx[j] = 32 * j + lane < n ? gw * __ldg(p.xg + t.row0 + c0 + 32 * j + lane) : 0.0f;
-            ok = warp_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
+            ok = warp_wait(smem_u32(&C.tfull), aphase, abort_flag);
             if (!ok) break;
             fence_after();
             Part<Tout> part;
-            part.take(tmem + ((uint32_t)(q * 32) << 16) + acc * T + c0, n);
+            part.take(tmem + ((uint32_t)(q * 32) << 16) + c0, n);
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty[acc]), 0));
-            if (++acc == S::kAcc) { acc = 0; aphase ^= 1; }
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty), 0));
+            aphase ^= 1;
             part.put(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn);
         }
         if (!ok) give_up(abort_flag);
@@ -603,32 +644,35 @@ bool make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int T, typename Tout>
+template <bool kSplit, typename Tout>
 lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
-                         const ProdArgs& p, int sms, cudaStream_t st) {
-    using S = Shape<T>;
+                         const ProdArgs& p, int parts, int sms, cudaStream_t st) {
+    using S = Shape;
     CUtensorMap wmap, xmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T))
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    const int64_t tiles = (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;  // at most
+    const int64_t tiles = (p.offsets ? p.n_rows / kT + p.G : (p.n_rows + kT - 1) / kT) * p.mtiles;  // at most
     if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
-    const size_t smem = (size_t)S::kStages * S::kStageBytes + 1024 + sizeof(Control<T>);
-    static_assert(S::kStages * S::kStageBytes + 1024 + (int)sizeof(Control<T>) <= 227 * 1024, "shared memory");
-    auto kernel = product_kernel<T, Tout>;
+    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 4 * kTurnBytes + 1024 + sizeof(Control);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    auto kernel = product_kernel<kSplit, Tout>;
     lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                               "product_kernel shared memory");
     if (s != LH_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.gridDim = dim3((unsigned)(kSplit ? tiles * parts : (tiles < sms ? tiles : sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = kSplit ? 2 : 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p), "product_kernel launch");
 }
 
@@ -643,22 +687,22 @@ bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int T, typename Tout>
+template <typename Tout>
 lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                       ProdArgs p, int sms, cudaStream_t st) {
     p.mtiles = (p.mtiles128 + 1) / 2;
-    const int64_t tiles = (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;
+    const int64_t tiles = (p.offsets ? p.n_rows / kPairT + p.G : (p.n_rows + kPairT - 1) / kPairT) * p.mtiles;
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "too many tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T / 2) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kPairT / 2) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    constexpr size_t smem = (size_t)Pair<T>::kStages * Pair<T>::kStageBytes + 8 * kTurnBytes + 1024 + sizeof(PairControl<T>);
+    constexpr size_t smem = (size_t)Pair::kStages * Pair::kStageBytes + 8 * kTurnBytes + 1024 + sizeof(PairControl);
     static_assert(smem <= 227 * 1024, "shared memory");
-    auto kernel = product_pair_kernel<T, Tout>;
+    auto kernel = product_pair_kernel<Tout>;
     lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                               "product_pair_kernel shared memory");
     if (s != LH_OK) return s;
@@ -677,6 +721,22 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_pair_kernel launch");
+}
+
+// Which kernel: CTA pairs where groups have rows for their tiles of 256 tokens; else
+// single CTAs, and while the tiles of one matrix leave half of the SMs idle, c_in split
+// over clusters.
+template <typename Tout>
+lh_status dispatch(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
+                   const ProdArgs& p, int sms, cudaStream_t st) {
+    if (p.n_rows >= kPairRows * p.G) return launch_pair<Tout>(encode, X, W, c_in, p, sms, st);
+    if (!p.offsets) {
+        const int64_t tiles = (p.n_rows + kT - 1) / kT * p.mtiles;
+        int parts = 1;
+        while (parts < 8 && tiles * parts * 2 <= sms && parts * 2 <= p.stages_k) parts *= 2;
+        if (parts > 1) return launch_product<true, Tout>(encode, X, W, c_in, p, parts, sms, st);
+    }
+    return launch_product<false, Tout>(encode, X, W, c_in, p, 1, sms, st);
 }
 
 lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets,
@@ -701,11 +761,12 @@ lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const 
 }  // namespace
 }  // namespace lh
 
-extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale,
-                                     const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale,
-                                     const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out,
-                                     int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, void* stream) {
-    using namespace lh;
+namespace lh {
+namespace {
+lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale, const uint8_t* W_packed,
+                 const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets, int64_t n_groups,
+                 int64_t n_rows, int64_t c_out, int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, bool early,
+                 void* stream) {
     clear_error();
     lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
     if (s != LH_OK) return s;
@@ -725,14 +786,21 @@ extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_s
     p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
     p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
     p.steps = (int)scale_steps(c_in);
-    p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y;
+    p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y; p.early = early;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (n_rows >= kPairRows * n_groups) {
-        if (out_dtype == LH_BF16) return launch_pair<PAIRT, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
-        return launch_pair<PAIRT, float>(encode, X_packed, W_packed, c_in, p, sms, st);
-    }
-    if (out_dtype == LH_BF16) return launch_product<128, __nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
-    return launch_product<128, float>(encode, X_packed, W_packed, c_in, p, sms, st);
+    if (out_dtype == LH_BF16) return dispatch<__nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
+    return dispatch<float>(encode, X_packed, W_packed, c_in, p, sms, st);
+}
+
+}  // namespace
+}  // namespace lh
+
+extern "C" lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale,
+                                     const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale,
+                                     const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out,
+                                     int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, void* stream) {
+    return lh::matmul(X_packed, X_scales, X_gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out,
+                      c_in, Y, out_dtype, ld_y, false, stream);
 }
 
 namespace lh {
@@ -783,8 +851,9 @@ extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_
     s = lh_quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
                            scales, gscale, nullptr, LH_F32, stream);
     if (s != LH_OK) return s;
-    return lh_nvfp4_matmul(packed, scales, gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in,
-                           Y, out_dtype, ld_y, stream);
+    // the quantisation, if it ran, waited for everything before it and writes the workspace alone
+    return matmul(packed, scales, gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y,
+                  out_dtype, ld_y, n_src > 0, stream);
 }
 
 extern "C" lh_status lh_nvfp4_status(void* stream) {

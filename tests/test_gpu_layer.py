@@ -344,7 +344,8 @@ def token_tiles(codes, off):
 
 SIZES = [(1, 1, 32), (1, 128, 256), (2, 130, 64), (7, 33, 96), (16, 128, 512), (31, 200, 224), (33, 129, 288),
          (100, 5, 1024), (128, 256, 4096), (129, 127, 320), (200, 640, 800), (257, 300, 1056), (513, 384, 2048),
-         (1, 4096, 4096), (3, 1536, 2080), (1000, 1100, 512)]
+         (1, 4096, 4096), (3, 1536, 2080), (1000, 1100, 512), (20, 12300, 96),
+         (60, 9700, 64), (1, 100, 17408), (32, 384, 8192), (33, 384, 8192), (90, 130, 17408 // 4)]
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
@@ -367,7 +368,8 @@ def test_product_of_whole_numbers_is_exact(cuda_ok, n, m, c, t):
 @pytest.mark.parametrize("counts,before,after,m,c", [
     ([1], 0, 0, 128, 256), ([0, 1, 0, 0, 3], 0, 0, 96, 64), ([5, 17, 130, 0, 1, 300], 0, 0, 200, 544),
     ([128, 256, 129], 2, 7, 257, 96), ([0] * 70 + [2, 1] + [0] * 30 + [33], 0, 5, 64, 128), ([0, 0], 4, 0, 32, 32),
-    ([1] * 100, 0, 0, 130, 1024), ([64, 31, 97, 255, 2], 1, 1, 384, 2048),
+    ([1] * 100, 0, 0, 130, 1024), ([300, 700, 0, 513, 16], 5, 3, 300, 352), ([1024, 1], 0, 0, 520, 128),
+    ([40, 0, 33, 2, 65], 0, 0, 70, 4352), ([64, 31, 97, 255, 2], 1, 1, 384, 2048),
 ])
 def test_grouped_product_of_whole_numbers_is_exact(cuda_ok, counts, before, after, m, c, t):
     rng = np.random.default_rng(len(counts) + m)
