@@ -60,11 +60,11 @@ struct Shape {
     // multiples of 4 columns, so a tile starts with a scale tile)
     static constexpr int kScaleCol = 2 * kT, kSetCols = 32, kTmemCols = 512;
     static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "TMEM columns");
-    static_assert(kStages * kStageBytes >= kT * kM * 4, "split: the partial sums reuse the ring");
+    static_assert(kStages * kStageBytes >= 2 * kT * kM * 4, "split: the partial sums reuse the ring");
 };
 
 struct Control {
-    uint64_t full[Shape::kStages], empty[Shape::kStages], tfull[2], tempty[2], drain;
+    uint64_t full[Shape::kStages], empty[Shape::kStages], tfull[2], tempty[2], done, sums;
     uint32_t tmem;
     int abort_flag;
 };
@@ -127,9 +127,22 @@ struct Walk {
     }
 };
 
-// mbar_wait with one answer for the warp: its lanes may see an expired limit apart.
+// Waits for the phase of `parity` with one answer for the warp; false after 1 s, or when
+// another warp gave up. The timer is read only after many tries: reading it takes longer
+// than most waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+    uint64_t t0 = 0;
+    bool ok = true;
+    for (uint32_t it = 1; !mbar_try(bar, parity); ++it) {
+        if ((it & 255) != 0) continue;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (*abort_flag || now - t0 > kTimeoutNs) {
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
 }
 __device__ __forceinline__ void give_up(volatile int* flag) {
     *flag = 1;
@@ -228,11 +241,13 @@ struct Part<__nv_bfloat16> {
 };
 
 // kSplit: a cluster of CTAs works on one tile, each on a part of c_in; the partial sums
-// meet in distributed shared memory, each CTA adding up those of 128 / cluster tokens in the
+// meet in distributed shared memory, each CTA adding up those of its share of the tokens in the
 // order of the parts (the same sums every time). Without it a CTA walks over whole tiles.
 template <bool kSplit, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
+                                                              const __grid_constant__ CUtensorMap wsmap,
+                                                              const __grid_constant__ CUtensorMap xsmap,
                                                               const ProdArgs p) {
     using S = Shape;
     extern __shared__ uint8_t smem_raw[];
@@ -255,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             mbar_init(smem_u32(&C.tfull[a]), 1);
             mbar_init(smem_u32(&C.tempty[a]), 4);
         }
-        mbar_init(smem_u32(&C.drain), 1);
+        mbar_init(smem_u32(&C.done), 1);
+        mbar_init(smem_u32(&C.sums), 1);
         C.abort_flag = 0;
         mbar_init_fence();
     }
@@ -276,15 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         bool ok = true;
         for (int u = first; ok && walk.find(p, u, t); u += step) {
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
-            const uint8_t* wsrc = p.ws + (t.g * p.mtiles + t.mt) * (int64_t)p.steps * kTileBytes;
-            const uint8_t* xsrc = p.xs + (group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps * (int64_t)kTileBytes;
+            const int wsrow = (int)((t.g * p.mtiles + t.mt) * p.steps);
+            const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
             const int boxes = (t.rows + kBox - 1) / kBox;
-            auto scale_bytes = [&](int ks) { return (p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4) * kTileBytes; };
+            const uint32_t bytes = S::kA + boxes * kBox * kRowBytes + S::kSa + S::kSb;
             auto weights = [&](int s, int ks) {
                 const uint32_t bar = smem_u32(&C.full[s]), a = ring + s * S::kStageBytes;
-                mbar_expect_tx(bar, S::kA + boxes * kBox * kRowBytes + 2 * scale_bytes(ks));
+                mbar_expect_tx(bar, bytes);
                 tma_load_2d(a, &wmap, ks * kRowBytes, wrow, bar);
-                bulk_load(a + S::kA + S::kB, wsrc + (int64_t)ks * 4 * kTileBytes, scale_bytes(ks), bar);
+                // past the last step this brings other scales, or zeros, that no product uses
+                tma_load_2d(a + S::kA + S::kB, &wsmap, 0, wsrow + 4 * ks, bar);
             };
             if (p.early && u == first) {
                 ahead = ks1 - ks0 < S::kStages ? ks1 - ks0 : S::kStages;
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     if (ahead == 0) weights(stage, ks);
                     for (int i = 0; i < boxes; ++i)
                         tma_load_2d(b + i * kBox * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * kBox, bar);
-                    bulk_load(b + S::kB + S::kSa, xsrc + (int64_t)ks * 4 * kTileBytes, scale_bytes(ks), bar);
+                    tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
                 }
                 __syncwarp();
                 if (ahead > 0) --ahead;
@@ -357,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         if (!ok) {  // the products in flight end before the CTA does
             give_up(abort_flag);
-            if (elect_one()) mma_commit(smem_u32(&C.drain));
+            if (elect_one()) mma_commit(smem_u32(&C.done));
             __syncwarp();
             int none = 0;
-            warp_wait(smem_u32(&C.drain), 0, &none);
+            warp_wait(smem_u32(&C.done), 0, &none);
         }
     } else if (!kSplit) {
         if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -393,39 +410,68 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (walk.find(p, first, t) && !warp_wait(smem_u32(&C.tfull[0]), 0, abort_flag)) give_up(abort_flag);
     }
     if constexpr (kSplit) {
-        // one tile: every CTA of the cluster is done with its ring, which now takes the
-        // sums, [part][its tokens][channel]
-        __syncwarp();
-        cluster_sync();
-        const int per = kT / parts, q = warp & 3;
-        float* sums = reinterpret_cast<float*>(base_p);
+        // One tile: the ring is idle once all its products are done. Its first 64 KB take
+        // this CTA's sums, [token][channel], the next 64 KB those of the other parts for this
+        // CTA's tokens, [part][token][channel], sent by bulk copies.
+        const int per = (t.rows + parts - 1) / parts, q = warp & 3;
+        float* mine = reinterpret_cast<float*>(base_p);
+        float* theirs = mine + kT * kM;
+        auto tokens_of = [&](int r) {  // how many of its tokens the tile has
+            const int n = t.rows - r * per;
+            return n < 0 ? 0 : (n < per ? n : per);
+        };
+        const int64_t row0 = t.row0 + rank * per;
+        float gx[2] = {0.0f, 0.0f};  // of this CTA's tokens, one per lane (two parts: 64 tokens)
         if (warp >= 2) {
+            const float gw = __ldg(p.wg + t.g);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (32 * j + lane < tokens_of(rank)) gx[j] = gw * __ldg(p.xg + row0 + 32 * j + lane);
             fence_after();
             for (int c = 0; c < t.rows; c += 32) {
                 uint32_t r[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, r);
                 tmem_wait32(r);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (c + i >= t.rows) break;
-                    const int to = (c + i) / per;
-                    const uint32_t at = smem_u32(sums + (rank * per + (c + i - to * per)) * kM + q * 32 + lane);
-                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr(at, to)), "r"(r[i]) : "memory");
-                }
+                for (int i = 0; i < 32; ++i) mine[(c + i) * kM + q * 32 + lane] = __uint_as_float(r[i]);
             }
+            fence_proxy_async();
         }
         __syncwarp();
         cluster_sync();
         if (warp >= 2) {
-            const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
-            const float gw = __ldg(p.wg + t.g);
-            for (int i = 0; i < per && rank * per + i < t.rows; ++i) {
-                const int64_t row = t.row0 + rank * per + i;
-                float v = 0.0f;
-                for (int s = 0; s < parts; ++s) v += sums[(s * per + i) * kM + q * 32 + lane];
-                if (ch < p.c_out) store_out(static_cast<Tout*>(p.Y) + row * p.ld_y + ch, v * (gw * __ldg(p.xg + row)));
+            const uint32_t bar = smem_u32(&C.sums), got = (parts - 1) * tokens_of(rank) * kM * 4;
+            if (warp == 2 && elect_one()) {
+                if (got) mbar_expect_tx(bar, got);
+                for (int r = 0; r < parts; ++r)
+                    if (r != rank && tokens_of(r) > 0)
+                        bulk_copy_cluster(cluster_addr(smem_u32(theirs + rank * per * kM), r), smem_u32(mine + r * per * kM),
+                                          tokens_of(r) * kM * 4, cluster_addr(bar, r));
+            }
+            __syncwarp();
+            if (got) {
+                if (!warp_wait(bar, 0, abort_flag)) give_up(abort_flag);
+                const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
+                Tout* y = static_cast<Tout*>(p.Y) + row0 * p.ld_y + ch;
+                const int n = tokens_of(rank);
+                for (int i0 = 0; i0 < n; i0 += 8) {  // the additions of eight tokens overlap
+                    float v[8] = {};
+                    for (int s = 0; s < parts; ++s) {
+                        const float* part = s == rank ? mine + rank * per * kM : theirs + s * per * kM;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i0 + i < n) v[i] += part[(i0 + i) * kM + q * 32 + lane];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float g = __shfl_sync(0xFFFFFFFFu, i0 < 32 ? gx[0] : gx[1], (i0 + i) & 31);
+                        if (i0 + i < n && ch < p.c_out) store_out(y + (int64_t)(i0 + i) * p.ld_y, v[i] * g);
+                    }
+                }
             }
         }
+        __syncwarp();
+        cluster_sync();  // nothing is in flight from or to a CTA that ends
     }
     fence_before();
     __syncthreads();
@@ -456,7 +502,7 @@ struct Pair {
 };
 
 struct PairControl {
-    uint64_t full[Pair::kStages], empty[Pair::kStages], tfull, tempty, drain;
+    uint64_t full[Pair::kStages], empty[Pair::kStages], tfull, tempty, done;
     uint32_t tmem;
     int abort_flag;
 };
@@ -484,7 +530,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         mbar_init(smem_u32(&C.tfull), 1);
         mbar_init(smem_u32(&C.tempty), 16);  // the epilogue warps of both CTAs
-        mbar_init(smem_u32(&C.drain), 1);
+        mbar_init(smem_u32(&C.done), 1);
         C.abort_flag = 0;
         mbar_init_fence();
     }
@@ -578,10 +624,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             if (!ok) {  // the products in flight end before the CTAs do
                 give_up(abort_flag);
-                if (elect_one()) mma_commit_pair(smem_u32(&C.drain));
+                if (elect_one()) mma_commit_pair(smem_u32(&C.done));
                 __syncwarp();
                 int none = 0;
-                warp_wait(smem_u32(&C.drain), 0, &none);
+                warp_wait(smem_u32(&C.done), 0, &none);
             }
         }
     } else {
@@ -644,13 +690,27 @@ bool make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as rows of 512 bytes: boxes of the four steps of a stage.
+bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* p, int64_t tiles) {
+    const cuuint64_t dims[2] = {kTileBytes / 4, (cuuint64_t)tiles};
+    const cuuint64_t strides[1] = {kTileBytes};
+    const cuuint32_t box[2] = {kTileBytes / 4, 4};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kSplit, typename Tout>
 lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                          const ProdArgs& p, int parts, int sms, cudaStream_t st) {
     using S = Shape;
-    CUtensorMap wmap, xmap;
+    const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
+    if (xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512) return fail(LH_ERR_UNSUPPORTED, "too many scale tiles");
+    CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox))
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox) ||
+        !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const int64_t tiles = (p.offsets ? p.n_rows / kT + p.G : (p.n_rows + kT - 1) / kT) * p.mtiles;  // at most
     if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
@@ -673,18 +733,7 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kSplit ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p), "product_kernel launch");
-}
-
-// Scale tiles as rows of 512 bytes: boxes of the four steps of a stage.
-bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const uint8_t* p, int64_t tiles) {
-    const cuuint64_t dims[2] = {kTileBytes / 4, (cuuint64_t)tiles};
-    const cuuint64_t strides[1] = {kTileBytes};
-    const cuuint32_t box[2] = {kTileBytes / 4, 4};
-    const cuuint32_t estr[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_kernel launch");
 }
 
 template <typename Tout>

@@ -147,12 +147,6 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Contiguous global -> shared copy (addresses and size multiples of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 // K-major operand in shared memory, rows of 128 bytes, 128-byte swizzle: groups of
 // 8 rows are 1024 bytes apart (stride byte offset 64 units of 16).
 __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
@@ -208,6 +202,15 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Shared memory of this CTA -> that of another of its cluster, reported to a barrier
+// there (addresses and size multiples of 16 bytes).
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
+                                                  uint32_t bar_cluster) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_cluster),
+        "r"(src), "r"(bytes), "r"(bar_cluster)
+        : "memory");
 }
 // Into this CTA's shared memory, reported to a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
