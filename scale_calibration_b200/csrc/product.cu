@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // whole accumulator into registers and free it before they scale and store.
 
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
-constexpr int kPairRows = 256;     // rows per group from which the pairs are taken
+constexpr int kPairRows = 192;     // rows per group from which groups are given to pairs
 
 constexpr int kPairT = 256;        // tokens of a pair's tile: two scale tiles
 
@@ -772,17 +772,20 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_pair_kernel launch");
 }
 
-// Which kernel: CTA pairs where groups have rows for their tiles of 256 tokens; else
-// single CTAs, and while the tiles of one matrix leave half of the SMs idle, c_in split
-// over clusters.
+// Which kernel. One matrix: CTA pairs above 128 tokens (160 x 4096 -> 12288: 13.1 us
+// against 16.1 us in two tiles of single CTAs; 128: 11.2 us single, 13.0 us in pairs), else
+// single CTAs, with c_in split over clusters while the tiles leave half of the SMs idle.
+// Groups, whose sizes the host does not know: pairs from 192 rows a group on (64 experts
+// 2048 -> 1536: 256 rows a group 54 us in pairs and 58 us in single CTAs, 128 rows a group
+// 42 and 39 us).
 template <typename Tout>
 lh_status dispatch(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                    const ProdArgs& p, int sms, cudaStream_t st) {
-    if (p.n_rows >= kPairRows * p.G) return launch_pair<Tout>(encode, X, W, c_in, p, sms, st);
+    if (p.offsets ? p.n_rows >= kPairRows * p.G : p.n_rows > kT)
+        return launch_pair<Tout>(encode, X, W, c_in, p, sms, st);
     if (!p.offsets) {
-        const int64_t tiles = (p.n_rows + kT - 1) / kT * p.mtiles;
         int parts = 1;
-        while (parts < 8 && tiles * parts * 2 <= sms && parts * 2 <= p.stages_k) parts *= 2;
+        while (parts < 8 && p.mtiles * parts * 2 <= sms && parts * 2 <= p.stages_k) parts *= 2;
         if (parts > 1) return launch_product<true, Tout>(encode, X, W, c_in, p, parts, sms, st);
     }
     return launch_product<false, Tout>(encode, X, W, c_in, p, 1, sms, st);
