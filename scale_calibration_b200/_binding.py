@@ -3,7 +3,8 @@
 Every function here has the name of the C entry point it calls and takes
 device pointers either as torch CUDA tensors or as integers. Nothing here
 computes any part of the calibration: all arithmetic runs in the library's
-kernels. If liblh.so is missing the import fails; there is no fallback.
+kernels. If liblh.so (or _lhcall.so, see csrc/pycall.c) is missing the import
+fails; there is no fallback.
 """
 from __future__ import annotations
 
@@ -257,34 +258,48 @@ def lh_search_amax(W, w_dtype, n_mats, c_out, c_in, ld_w, global_amax, H, best_a
     return s
 
 
+# The calls of a step of inference, where the host's microseconds count, go through
+# _lhcall (arguments by kind: p pointer, i integer, t dtype, s stream).
+def _fast(name: str, kinds: str):
+    from . import _lhcall
+    return _lhcall.Call(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value, kinds, _dtype, _stream)
+
+
+_route_tokens = _fast("lh_route_tokens", "piiippps")
+_gather_tokens = _fast("lh_gather_tokens", "ptiiipiipis")
+_combine_tokens = _fast("lh_combine_tokens", "ptiiippiipis")
+_combine_tokens_grad = _fast("lh_combine_tokens_grad", "ptiiiipiipppips")
+_quantize_tokens = _fast("lh_quantize_tokens", "ptiiipiipipppppts")
+_nvfp4_matmul = _fast("lh_nvfp4_matmul", "pppppppiiiiptis")
+_nvfp4_linear = _fast("lh_nvfp4_linear", "ptiiipiipippppiptipis")
+
+
 def lh_route_tokens(ids, n_tok, k, n_experts, offsets, order, pos, stream=None, check=True) -> int:
-    s = _lib.lh_route_tokens(_ptr(ids), n_tok, k, n_experts, _ptr(offsets), _ptr(order), _ptr(pos), _stream(stream))
-    if check:
+    s = _route_tokens(ids, n_tok, k, n_experts, offsets, order, pos, stream)
+    if s and check:
         _check(s, "lh_route_tokens")
     return s
 
 
 def lh_gather_tokens(X, dtype, n_tok, c, ld_x, order, k, n_rows, Xs, ld_xs, stream=None, check=True) -> int:
-    s = _lib.lh_gather_tokens(_ptr(X), _dtype(dtype), n_tok, c, ld_x, _ptr(order), k, n_rows, _ptr(Xs), ld_xs,
-                              _stream(stream))
-    if check:
+    s = _gather_tokens(X, dtype, n_tok, c, ld_x, order, k, n_rows, Xs, ld_xs, stream)
+    if s and check:
         _check(s, "lh_gather_tokens")
     return s
 
 
 def lh_combine_tokens(Ys, dtype, n_rows, c, ld_ys, pos, weights, n_tok, k, Y, ld_y, stream=None, check=True) -> int:
-    s = _lib.lh_combine_tokens(_ptr(Ys), _dtype(dtype), n_rows, c, ld_ys, _ptr(pos), _ptr(weights), n_tok, k, _ptr(Y),
-                               ld_y, _stream(stream))
-    if check:
+    s = _combine_tokens(Ys, dtype, n_rows, c, ld_ys, pos, weights, n_tok, k, Y, ld_y, stream)
+    if s and check:
         _check(s, "lh_combine_tokens")
     return s
 
 
 def lh_combine_tokens_grad(dY, dtype, n_tok, k, c, ld_dy, Ys, ld_ys, n_rows, pos, weights, dYs, ld_dys, dweights,
                            stream=None, check=True) -> int:
-    s = _lib.lh_combine_tokens_grad(_ptr(dY), _dtype(dtype), n_tok, k, c, ld_dy, _ptr(Ys), ld_ys, n_rows, _ptr(pos),
-                                    _ptr(weights), _ptr(dYs), ld_dys, _ptr(dweights), _stream(stream))
-    if check:
+    s = _combine_tokens_grad(dY, dtype, n_tok, k, c, ld_dy, Ys, ld_ys, n_rows, pos, weights, dYs, ld_dys, dweights,
+                             stream)
+    if s and check:
         _check(s, "lh_combine_tokens_grad")
     return s
 
@@ -306,20 +321,18 @@ def lh_nvfp4_tile_scales(block_scales, n_mats, c_out, c_in, tiles, stream=None, 
 
 def lh_quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
                        scale_tiles, token_scale, X_out=None, out_dtype=LH_BF16, stream=None, check=True) -> int:
-    s = _lib.lh_quantize_tokens(_ptr(X), _dtype(x_dtype), n_src, c_in, ld_x, _ptr(rows), row_div, n_rows,
-                                _ptr(offsets), n_groups, _ptr(global_amax), _ptr(packed), _ptr(scale_tiles),
-                                _ptr(token_scale), _ptr(X_out), _dtype(out_dtype), _stream(stream))
-    if check:
+    s = _quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
+                         scale_tiles, token_scale, X_out, out_dtype, stream)
+    if s and check:
         _check(s, "lh_quantize_tokens")
     return s
 
 
 def lh_nvfp4_matmul(X_packed, X_scales, X_gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in,
                     Y, out_dtype, ld_y, stream=None, check=True) -> int:
-    s = _lib.lh_nvfp4_matmul(_ptr(X_packed), _ptr(X_scales), _ptr(X_gscale), _ptr(W_packed), _ptr(W_scales),
-                             _ptr(W_gscale), _ptr(offsets), n_groups, n_rows, c_out, c_in, _ptr(Y), _dtype(out_dtype),
-                             ld_y, _stream(stream))
-    if check:
+    s = _nvfp4_matmul(X_packed, X_scales, X_gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out,
+                      c_in, Y, out_dtype, ld_y, stream)
+    if s and check:
         _check(s, "lh_nvfp4_matmul")
     return s
 
@@ -335,9 +348,8 @@ def lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups) -> int:
 def lh_nvfp4_linear(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, W_packed,
                     W_scales, W_gscale, c_out, Y, out_dtype, ld_y, workspace, workspace_bytes, stream=None,
                     check=True) -> int:
-    s = _lib.lh_nvfp4_linear(_ptr(X), _dtype(x_dtype), n_src, c_in, ld_x, _ptr(rows), row_div, n_rows, _ptr(offsets),
-                             n_groups, _ptr(global_amax), _ptr(W_packed), _ptr(W_scales), _ptr(W_gscale), c_out,
-                             _ptr(Y), _dtype(out_dtype), ld_y, _ptr(workspace), workspace_bytes, _stream(stream))
-    if check:
+    s = _nvfp4_linear(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, W_packed,
+                      W_scales, W_gscale, c_out, Y, out_dtype, ld_y, workspace, workspace_bytes, stream)
+    if s and check:
         _check(s, "lh_nvfp4_linear")
     return s

@@ -1,4 +1,5 @@
-"""Builds liblh.so (the CUDA library behind include/lh.h) for sm_100a.
+"""Builds liblh.so (the CUDA library behind include/lh.h) for sm_100a, and the
+small CPython extension that calls it (_lhcall.so).
 
     python scale_calibration_b200/build.py [--verbose] [--counters]
 
@@ -12,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +29,20 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+# The Python side's call path (csrc/pycall.c), a plain CPython extension.
+CALL_SRC = os.path.join(CSRC, "pycall.c")
+CALL_LIB = os.path.join(PKG, "_lhcall.so")
+
+
+def build_call(force: bool = False) -> str:
+    if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < os.path.getmtime(CALL_SRC):
+        tmp = CALL_LIB + f".tmp{os.getpid()}"
+        subprocess.check_call([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-fPIC", "-shared", "-fvisibility=hidden",
+                               "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp])
+        os.replace(tmp, CALL_LIB)
+    return CALL_LIB
 
 
 # The measurement build: the same sources with the sweep's work counters compiled in
@@ -60,6 +76,7 @@ def _build_lib(lib: str, objdir: str, defines: list[str], verbose: bool) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_call(force)
     if not force and not _stale_lib(LIB):
         return LIB
     return _build_lib(LIB, os.path.join(PKG, "_build"), [], verbose)

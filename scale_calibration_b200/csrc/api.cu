@@ -39,6 +39,18 @@ int sm_count() {
     return cache[dev];
 }
 
+lh_status allow_shared(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    lh_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+    if (s != LH_OK) return s;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;  // beyond: asked every time
+    if (done.load(std::memory_order_relaxed) & bit) return LH_OK;
+    s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+                    "dynamic shared memory");
+    if (s == LH_OK) done.fetch_or(bit, std::memory_order_relaxed);
+    return s;
+}
+
 }  // namespace lh
 
 extern "C" const char* lh_status_string(lh_status s) {

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "lh.h"
 
 namespace lh {
@@ -23,6 +25,9 @@ inline bool valid_dtype(int t) { return t == LH_BF16 || t == LH_F32; }
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device; `done` (one
+// static word per kernel, a bit per device) keeps later calls from asking again.
+lh_status allow_shared(const void* kernel, size_t bytes, std::atomic<uint64_t>& done);
 
 // ---------------------------------------------------------------- device side
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t h) {

@@ -426,11 +426,9 @@ extern "C" lh_status lh_route_tokens(const int32_t* ids, int64_t n_tok, int64_t 
     if (sm_count() <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     const int n = (int)(n_tok * k), E = (int)n_experts;
     const size_t smem = (size_t)(kRouteWarps + 2) * E * sizeof(uint32_t);
-    if (smem > 48 * 1024) {
-        s = cuda_status(cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                        "route_kernel shared memory");
-        if (s != LH_OK) return s;
-    }
+    static std::atomic<uint64_t> done{0};  // for the largest number of experts
+    s = allow_shared((const void*)route_kernel, (size_t)(kRouteWarps + 2) * kMaxExperts * sizeof(uint32_t), done);
+    if (s != LH_OK) return s;
     // one CTA walks 4096 ids in 4 steps of its warps; more ids want the cluster's eight SMs
     const unsigned ctas = n <= 4 * kRouteThreads ? 1 : kRouteCluster;
     cudaLaunchConfig_t cfg = {};

@@ -717,8 +717,8 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 4 * kTurnBytes + 1024 + sizeof(Control);
     static_assert(smem <= 227 * 1024, "shared memory");
     auto kernel = product_kernel<kSplit, Tout>;
-    lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                              "product_kernel shared memory");
+    static std::atomic<uint64_t> done{0};
+    lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(kSplit ? tiles * parts : (tiles < sms ? tiles : sms)));
@@ -752,8 +752,8 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     constexpr size_t smem = (size_t)Pair::kStages * Pair::kStageBytes + 8 * kTurnBytes + 1024 + sizeof(PairControl);
     static_assert(smem <= 227 * 1024, "shared memory");
     auto kernel = product_pair_kernel<Tout>;
-    lh_status s = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                              "product_pair_kernel shared memory");
+    static std::atomic<uint64_t> done{0};
+    lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
     const int64_t pairs = sms / 2;
     cudaLaunchConfig_t cfg = {};
