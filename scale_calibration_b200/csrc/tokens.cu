@@ -20,12 +20,13 @@ template <typename T>
 constexpr int kHeld = 8 / (int)sizeof(T);
 
 struct TokenArgs {
-    int64_t n_src, ld, n_rows, G, J, steps;
-    uint32_t row_div;
-    const int* rows;         // source of each row (over row_div), or null
-    const int64_t* offsets;  // groups of rows, or null
-    const float* gamax;      // amax of the tensor, or null (per token)
-    bool wide_in, wide_out;  // rows of X, X_out 32-byte aligned
+    int64_t n_src, ld;
+    int n_rows, G, J, steps;
+    uint32_t div_mul, div_shift;  // f / row_div = umulhi(f, div_mul) >> div_shift for f < 2^31; mul 0: row_div 1
+    const int* rows;              // source of each row (over row_div), or null
+    const int64_t* offsets;       // groups of rows, or null
+    const float* gamax;           // amax of the tensor, or null (per token)
+    bool wide_in, wide_out;       // rows of X, X_out 32-byte aligned
     uint8_t* packed;
     uint8_t* tiles;
     float* gscale;
@@ -33,22 +34,22 @@ struct TokenArgs {
 
 // Largest group g with offsets[g] <= row, by the whole warp, 32 offsets a round; false
 // when the row lies in no group.
-__device__ __forceinline__ bool find_group(const TokenArgs& p, int64_t row, int64_t& g, int64_t& lo) {
+__device__ __forceinline__ bool find_group(const TokenArgs& p, int row, int& g, int& lo) {
     g = 0;
     lo = 0;
     if (!p.offsets) return true;
     const int lane = threadIdx.x & 31;
-    int64_t span = p.G;  // offsets[g] <= row < offsets[g + span], if there is such a group
+    int span = p.G;  // offsets[g] <= row < offsets[g + span], if there is such a group
     while (span > 1) {
-        const int64_t step = (span + 31) / 32;
+        const int step = (span + 31) >> 5;
         const bool le = lane * step < span && __ldg(p.offsets + g + lane * step) <= row;
         const uint32_t hit = __ballot_sync(0xFFFFFFFFu, le);
         const int l = hit ? 31 - __clz(hit) : 0;
         g += l * step;
-        span = span - l * step < step ? span - l * step : step;
+        span = min(span - l * step, step);
     }
-    lo = __ldg(p.offsets + g);
-    lo = lo < 0 ? 0 : lo;
+    const int64_t first = __ldg(p.offsets + g);
+    lo = first < 0 ? 0 : (int)min(first, (int64_t)INT_MAX);
     return lo <= row && row < __ldg(p.offsets + g + 1);
 }
 
@@ -132,15 +133,21 @@ __device__ __forceinline__ void store16(float* p, const float (&o)[16], bool wid
 // division: with g in [2^-85, 2^100], q = RN(a y) and RN(q + (a - q g) y) with y = RN(1/g)
 // is the correctly rounded a / g for |a| >= 2^-100 (P. Markstein, IBM J. Res. Dev. 34(1),
 // 1990: the residual is exact), and a smaller a gives less than 2^-14 either way, code 1.
-// The same holds for a / 6.
+// The same holds for a / 6, and for g itself.
 struct RowScale {
     float g, ny, nan;
     bool fast;
-    __device__ explicit RowScale(float gs) {
-        g = gs;
+    // From an amax >= 0 (or NaN).
+    __device__ explicit RowScale(float amax) {
         nan = __int_as_float(0x7FFFFFFF);
-        fast = gs >= 2.584939e-26f && gs <= 1.2676506e30f;
-        ny = fast ? -__frcp_rn(gs) : 0.0f;
+        fast = amax >= 6.948286e-23f && amax <= 3.3230700e33f;  // 2688 * [2^-85, 2^100], rounded inwards
+        if (fast) {
+            g = quotient(amax, 2688.0f, -1.0f / 2688.0f);
+            ny = -__frcp_rn(g);
+        } else {
+            g = __fdiv_rn(amax, 2688.0f);
+            ny = 0.0f;
+        }
     }
     __device__ static float quotient(float a, float d, float nyd) {
         const float nq = __fmul_rn(a, nyd);          // -q
@@ -148,10 +155,15 @@ struct RowScale {
         return -__fmaf_rn(r, nyd, nq);
     }
     // E4M3 code of a block whose largest |x| is a, and the block's scale.
+    // kGiven: a may be above the row's amax.
+    template <bool kGiven>
     __device__ uint32_t code(float a, float& s) const {
         uint32_t c = 1;
         if (fast)
-            c = (uint32_t)e4m3_rne_code(quotient(quotient(a, 6.0f, -0.16666667f), g, ny));
+            {
+            const float sixth = quotient(a, 6.0f, -1.0f / 6.0f);
+            c = (uint32_t)e4m3_rne_code(quotient(kGiven ? fminf(sixth, 512.0f * g) : sixth, g, ny));  // above: the largest code
+        }
         else if (g != 0.0f)
             c = (uint32_t)e4m3_rne_code(__fdiv_rn(__fdiv_rn(a, 6.0f), g));
         c = c < 1 ? 1 : c;
@@ -166,7 +178,8 @@ struct RowScale {
 // row and keeps them, the warps agree on the row's largest |x|, and the blocks are
 // quantised from the registers; rows too wide for that are read twice (from L2). With a
 // given scale one pass does.
-template <typename Tin, typename Tout, bool kOut, int kWarps>
+// kGiven: the amax of the tensor is given.
+template <typename Tin, typename Tout, bool kOut, bool kGiven, int kWarps>
 __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
     tokens_kernel(const Tin* __restrict__ X, TokenArgs p, Tout* __restrict__ out) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -176,7 +189,7 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
     constexpr int kN = kHeld<Tin>;
     __shared__ uint32_t red[kRows][kWarps];
     const int tid = threadIdx.x % kSpan, part = threadIdx.x / kSpan, warp = tid >> 5, lane = tid & 31;
-    const int J = (int)p.J;
+    const int J = p.J;
     auto row_max = [&](uint32_t m) {
         m = __reduce_max_sync(0xFFFFFFFFu, m);
         if constexpr (kWarps > 1) {
@@ -188,23 +201,20 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
         }
         return m;
     };
-    for (int64_t row = (int64_t)blockIdx.x * kRows + part; row < p.n_rows; row += (int64_t)gridDim.x * kRows) {
-        int64_t g, lo;
+    for (int row = blockIdx.x * kRows + part; row < p.n_rows; row += gridDim.x * kRows) {
+        int g, lo;
         if (!find_group(p, row, g, lo)) continue;
         int64_t src = row;
         if (p.rows) {
             const int f = __ldg(p.rows + row);
-            src = f < 0 ? -1 : (int64_t)((uint32_t)f / p.row_div);
+            src = f < 0 ? -1 : (int64_t)(p.div_mul ? __umulhi((uint32_t)f, p.div_mul) >> p.div_shift : (uint32_t)f);
         }
         if (src < 0 || src >= p.n_src) continue;
         const Tin* x = X + src * p.ld;
         Held<Tin> h[kN];
         uint32_t bb[kN], mb = 0;
-        float gs;
         bool reload = true;
-        if (p.gamax) {
-            gs = __fdiv_rn(__ldg(p.gamax), 2688.0f);
-        } else {
+        if constexpr (!kGiven) {
             for (int j0 = tid; j0 - tid < J; j0 += kSpan * kN) {
 #pragma unroll
                 for (int i = 0; i < kN; ++i)
@@ -216,14 +226,15 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
                 }
             }
             mb = row_max(mb);
-            gs = __fdiv_rn(__uint_as_float(mb), 2688.0f);
             reload = J > kSpan * kN;
         }
         const bool bad_token = mb >= 0x7F800000u;
-        const RowScale rs(gs);
-        const int64_t r = row - lo;
-        uint8_t* tiles = p.tiles + scale_offset(group_tile(lo, g) + r / kTileRows, (int)(r % kTileRows), 0, p.steps);
-        for (int j0 = tid; j0 - tid < 4 * (int)p.steps; j0 += kSpan * kN) {
+        const RowScale rs(kGiven ? __ldg(p.gamax) : __uint_as_float(mb));
+        const uint32_t r = row - lo, rt = r % kTileRows;
+        uint8_t* tiles = p.tiles + (uint64_t)((uint32_t)lo / kTileRows + g + r / kTileRows) * (uint32_t)(p.steps * kTileBytes) +
+                         (rt % 32) * 16 + rt / 32 * 4;
+        const int64_t out0 = (int64_t)row * J;
+        for (int j0 = tid; j0 - tid < 4 * p.steps; j0 += kSpan * kN) {
             if (reload) {
 #pragma unroll
                 for (int i = 0; i < kN; ++i)
@@ -237,11 +248,11 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int j = j0 + i * kSpan;
-                if (j - lane >= 4 * (int)p.steps) break;  // the same for the warp
+                if (j - lane >= 4 * p.steps) break;  // the same for the warp
                 uint32_t code = 0;
                 if (j < J) {
                     float s;
-                    code = rs.code(__uint_as_float(bb[i]), s);
+                    code = rs.template code<kGiven>(__uint_as_float(bb[i]), s);
                     if (bb[i] >= 0x7F800000u || bad_token) {
                         code = 0x7F;
                         s = rs.nan;
@@ -249,20 +260,28 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
                     float w[16], o[16];
                     uint32_t word[2];
                     h[i].floats(w);
+                    if constexpr (kGiven) {
+                        // far above the amax, the quotients of quantize_block would overflow
+                        const float far = 1.1529215e18f * s;
+                        if (s >= 2.524355e-29f && __uint_as_float(bb[i]) > far) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = fminf(fmaxf(w[e], -far), far);
+                        }
+                    }
                     quantize_block<kOut, true>(w, s, o, word);
-                    reinterpret_cast<uint2*>(p.packed)[row * J + j] = make_uint2(word[0], word[1]);
-                    if constexpr (kOut) store16(out + (row * J + j) * 16, o, p.wide_out);
+                    reinterpret_cast<uint2*>(p.packed)[out0 + j] = make_uint2(word[0], word[1]);
+                    if constexpr (kOut) store16(out + (out0 + j) * 16, o, p.wide_out);
                 }
                 // the four codes of a step, one word of the tile
                 uint32_t v = code << (8 * (j & 3));
                 v |= __shfl_xor_sync(0xFFFFFFFFu, v, 1);
                 v |= __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-                if ((j & 3) == 0 && j < 4 * (int)p.steps)
+                if ((j & 3) == 0 && j < 4 * p.steps)
                     *reinterpret_cast<uint32_t*>(tiles + (int64_t)(j >> 2) * kTileBytes) = v;
             }
         }
-        if (p.gamax) mb = row_max(mb);
-        if (tid == 0) p.gscale[row] = mb >= 0x7F800000u ? rs.nan : gs;
+        if constexpr (kGiven) mb = row_max(mb);
+        if (tid == 0) p.gscale[row] = mb >= 0x7F800000u ? rs.nan : rs.g;
     }
 }
 
@@ -287,7 +306,7 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restr
     }
 }
 
-template <typename Tin, typename Tout, bool kOut, int kWarps>
+template <typename Tin, typename Tout, bool kOut, bool kGiven, int kWarps>
 lh_status launch_tokens_w(const void* X, const TokenArgs& p, void* out, int sms, cudaStream_t st) {
     constexpr int kRows = 8 / kWarps;
     const int64_t need = (p.n_rows + kRows - 1) / kRows, cap = (int64_t)sms * 16;
@@ -300,24 +319,31 @@ lh_status launch_tokens_w(const void* X, const TokenArgs& p, void* out, int sms,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, tokens_kernel<Tin, Tout, kOut, kWarps>, (const Tin*)X, p, (Tout*)out),
+    return cuda_status(cudaLaunchKernelEx(&cfg, tokens_kernel<Tin, Tout, kOut, kGiven, kWarps>, (const Tin*)X, p, (Tout*)out),
                        "tokens_kernel launch");
+}
+
+template <typename Tin, typename Tout, bool kOut, bool kGiven>
+lh_status launch_tokens_g(const void* X, const TokenArgs& p, void* out, int sms, cudaStream_t st) {
+    // enough warps to hold the row (its own scale); more while there are few, which with a
+    // given scale costs no reduction: up to 128 an SM, so that the loads in flight cover the
+    // memory's latency (1777 x 17408 f32: 60 us with 16, 47 us with 128)
+    int warps = 1;
+    while (warps < 8 && ((!kGiven && p.J > 32 * kHeld<Tin> * warps) ||
+                         (p.J > 32 * warps && p.n_rows * warps * 2 <= (kGiven ? 128 : 16) * (int64_t)sms)))
+        warps *= 2;
+    switch (warps) {
+        case 1: return launch_tokens_w<Tin, Tout, kOut, kGiven, 1>(X, p, out, sms, st);
+        case 2: return launch_tokens_w<Tin, Tout, kOut, kGiven, 2>(X, p, out, sms, st);
+        case 4: return launch_tokens_w<Tin, Tout, kOut, kGiven, 4>(X, p, out, sms, st);
+        default: return launch_tokens_w<Tin, Tout, kOut, kGiven, 8>(X, p, out, sms, st);
+    }
 }
 
 template <typename Tin, typename Tout, bool kOut>
 lh_status launch_tokens_o(const void* X, const TokenArgs& p, void* out, int sms, cudaStream_t st) {
-    // enough warps to hold the row (its own scale), and while the rows leave SMs idle
-    // enough to load it in one go
-    int warps = 1;
-    while (warps < 8 && ((!p.gamax && p.J > 32 * kHeld<Tin> * warps) ||
-                         (p.J > 32 * warps && p.n_rows * warps * 2 <= 16 * (int64_t)sms)))
-        warps *= 2;
-    switch (warps) {
-        case 1: return launch_tokens_w<Tin, Tout, kOut, 1>(X, p, out, sms, st);
-        case 2: return launch_tokens_w<Tin, Tout, kOut, 2>(X, p, out, sms, st);
-        case 4: return launch_tokens_w<Tin, Tout, kOut, 4>(X, p, out, sms, st);
-        default: return launch_tokens_w<Tin, Tout, kOut, 8>(X, p, out, sms, st);
-    }
+    return p.gamax ? launch_tokens_g<Tin, Tout, kOut, true>(X, p, out, sms, st)
+                   : launch_tokens_g<Tin, Tout, kOut, false>(X, p, out, sms, st);
 }
 
 template <typename Tin>
@@ -375,6 +401,8 @@ extern "C" lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t
     if (n_src < 0 || n_rows < 0 || c_in < 0 || n_groups < 1)
         return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
     if (row_div < 1) return fail(LH_ERR_INVALID_ARG, "row_div must be >= 1");
+    if (n_rows > INT_MAX - 512 || n_groups > INT_MAX - 512)
+        return fail(LH_ERR_UNSUPPORTED, "n_rows and n_groups must be below 2^31 - 512");
     if (row_div > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "row_div must be below 2^31");
     if (!rows && (row_div != 1 || n_rows > n_src))
         return fail(LH_ERR_INVALID_ARG, "without rows, row_div must be 1 and n_rows at most n_src");
@@ -392,8 +420,12 @@ extern "C" lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     TokenArgs p;
-    p.n_src = n_src; p.ld = ld_x; p.row_div = (uint32_t)row_div; p.n_rows = n_rows;
-    p.G = n_groups; p.J = c_in / 16; p.steps = scale_steps(c_in);
+    p.n_src = n_src; p.ld = ld_x; p.n_rows = (int)n_rows;
+    p.G = (int)n_groups; p.J = (int)(c_in / 16); p.steps = (int)scale_steps(c_in);
+    p.div_shift = 0;  // with 2^(s-1) < row_div <= 2^s: ceil(2^(31+s) / row_div), exact for 31-bit dividends
+    while ((int64_t(1) << p.div_shift) < row_div) ++p.div_shift;
+    p.div_mul = row_div == 1 ? 0u : (uint32_t)(((uint64_t(1) << (31 + p.div_shift)) + row_div - 1) / row_div);
+    if (row_div > 1) --p.div_shift;
     p.rows = (const int*)rows; p.offsets = offsets; p.gamax = global_amax;
     p.wide_in = (reinterpret_cast<uintptr_t>(X) & 31) == 0 && (ld_x * elem_bytes(x_dtype)) % 32 == 0;
     p.wide_out = (reinterpret_cast<uintptr_t>(X_out) & 31) == 0;

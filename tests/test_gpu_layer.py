@@ -241,6 +241,45 @@ def test_tokens_match_the_oracle(cuda_ok, n, c, mode, t):
     assert torch.equal(vb.cpu().view(torch.int16), torch.from_numpy(rv).to(torch.bfloat16).view(torch.int16))
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("amax", [0.0, 1e-42, 1e-37, 1e-30, 1e-20, 1.0, 1e20, 3e33, 3e38])
+def test_tokens_far_from_the_given_amax(cuda_ok, amax, t):
+    # every order of magnitude against scales at both ends of the range: they saturate, or vanish, with their signs
+    rng = np.random.default_rng(3)
+    v = np.ldexp(rng.choice([-1.0, 1.0], (60, 64)) * (1 + rng.random((60, 64))), np.arange(-126, 114, 4)[:, None])
+    x = torch.from_numpy(v.astype(np.float32)).to(DT[t])
+    a = np.float32(amax)
+    packed, tiles, g, values = quantize(x.cuda(), 60, 64, amax=torch.tensor([a], device="cuda"), out=torch.float32)
+    rp, rc, rg, rv = ref.quantize_tokens(x.float().numpy(), a)
+    assert np.array_equal(packed.cpu().numpy(), rp)
+    assert np.array_equal(ref.untile(tiles.cpu().numpy(), 60, 4), rc)
+    assert np.array_equal(g.cpu().numpy(), rg) and np.array_equal(values.cpu().numpy(), rv)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_tokens_of_every_magnitude(cuda_ok, t):
+    # each token's own scale, from the smallest numbers to the largest
+    rng = np.random.default_rng(4)
+    v = np.ldexp(rng.standard_normal((270, 48)), np.arange(-148, 122)[:, None])
+    x = torch.from_numpy(v.astype(np.float32)).to(DT[t])
+    packed, tiles, g, values = quantize(x.cuda(), 270, 48, out=torch.float32)
+    rp, rc, rg, rv = ref.quantize_tokens(x.float().numpy())
+    assert np.array_equal(packed.cpu().numpy(), rp)
+    assert np.array_equal(ref.untile(tiles.cpu().numpy(), 270, 3)[:, :3], rc)
+    assert np.array_equal(g.cpu().numpy(), rg) and np.array_equal(values.cpu().numpy(), rv)
+
+
+@pytest.mark.parametrize("div", [1, 2, 3, 5, 6, 7, 8, 31, 1000])
+def test_rows_over_their_divisor(cuda_ok, div):
+    rng = np.random.default_rng(div)
+    n_src, c = 37, 32
+    x = torch.from_numpy(rng.standard_normal((n_src, c)).astype(np.float32)).cuda()
+    src = rng.integers(0, n_src * div, 500).astype(np.int32)
+    packed, _, _, _ = quantize(x, n_src, c, torch.from_numpy(src).cuda(), div, 500)
+    rp, _, _, _ = ref.quantize_tokens(x.cpu().numpy()[src // div])
+    assert np.array_equal(packed.cpu().numpy(), rp)
+
+
 @pytest.mark.parametrize("counts,before,after", [([5, 0, 130, 1, 0], 0, 0), ([128, 128], 3, 9), ([0, 0, 1], 0, 200),
                                                  ([127, 129, 257], 1, 0)])
 def test_grouped_and_gathered_tokens(cuda_ok, counts, before, after):
@@ -549,6 +588,44 @@ def test_a_layer_of_experts(cuda_ok, n, k, e, m, c, t):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(once, y)
+    assert lh.lh_nvfp4_status() == 0
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("tensor", [False, True])
+@pytest.mark.parametrize("n,k,c,kind", [(1100, 4, 96, "route"), (1100, 4, 4128, "route"), (2100, 2, 544, "twice"),
+                                        (520, 8, 2080, "holes"), (140, 32, 64, "route"), (1400, 3, 9248, "twice")])
+def test_linear_of_tokens_with_several_rows(cuda_ok, n, k, c, kind, tensor, t):
+    # one call equals the two calls it stands for, row by row, whatever rows name the tokens' slots
+    lh = _lh()
+    rng = np.random.default_rng(n + k)
+    e, m = 7, 72
+    R = n * k
+    x = torch.from_numpy(rng.standard_normal((n, c)).astype(np.float32)).to(DT[t]).cuda()
+    x[3, c // 2] = float("nan")
+    w, _, _ = bank(rng, e, m, c)
+    ids = rng.integers(0, e, (n, k)).astype(np.int32)
+    if kind == "holes":
+        ids[rng.random((n, k)) < 0.3] = -1
+    off, order, _ = ref.route(ids, e)
+    src = order.copy()
+    if kind == "twice":  # several rows name one slot, some slots have none, some rows name nothing
+        src[:R] = rng.integers(-1, R + 9, R)
+        src[10:20] = 5
+        off[0], off[-1] = 3, R - 17
+    amax = torch.tensor([3.0], device="cuda") if tensor else None
+    sd, od = torch.from_numpy(src).cuda(), torch.from_numpy(off).cuda()
+    y = torch.full((R, pitch(m, t)), 4.0, dtype=DT[t], device="cuda")
+    linear(x, n, c, w, m, y, rows=sd, row_div=k, n_rows=R, off=od, amax=amax)
+    packed, tiles, g, _ = quantize(x, n, c, sd, k, R, od, amax)
+    y2 = torch.full_like(y, 4.0)
+    matmul(packed, tiles, g, *w, od, y2, m, c)
+    rows = np.arange(R)
+    inside = (rows >= off[0]) & (rows < off[-1])
+    named = inside & (src >= 0) & (src < R)
+    a, b = y.float().cpu().numpy()[named], y2.float().cpu().numpy()[named]
+    assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.nan_to_num(a), np.nan_to_num(b))
+    assert (y[torch.from_numpy(~inside).cuda()] == 4.0).all()
     assert lh.lh_nvfp4_status() == 0
 
 
