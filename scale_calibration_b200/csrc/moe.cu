@@ -38,58 +38,91 @@ __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) 
 
 // A stable counting sort in one launch: one cluster, each CTA a contiguous chunk of
 // the ids, each warp a contiguous run of its chunk. Every warp counts its run into a
-// histogram of its own (lanes with the same expert find one another with match.any,
-// the first of them adds), the counts become prefixes over warps, CTAs (through
-// distributed shared memory) and experts, and every warp walks its run again and
-// hands out places in order. No atomics: the order is that of the flat index.
+// histogram of its own (lanes with the same expert find one another by a ballot for each
+// bit of its number, the first of them adds; match.any, which does that in one instruction,
+// takes longer than them all: 4096 ids 8.2 us), which also gives each id its rank in the run; the counts
+// become prefixes over warps, CTAs (through distributed shared memory) and experts, and
+// the ids take their places. No atomics: the order is that of the flat index. What
+// bounds it is the chain of these steps, not the bytes; ranks stay in registers for the
+// first kHeldIds of a lane, the others wait in pos.
+constexpr int kHeldIds = 4;
+
 __global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __restrict__ ids, int n, int E,
                                                                  int64_t* __restrict__ offsets,
                                                                  int* __restrict__ order, int* __restrict__ pos) {
     extern __shared__ uint32_t sm[];
+    const int stride = E | 1;      // odd: a column of the histograms touches every bank
     uint32_t* total = sm;          // [E] this CTA's count per expert
     uint32_t* base = total + E;    // [E] first place of this CTA's rows of an expert
-    uint32_t* hist = base + E;     // [warps][E]
+    uint32_t* hist = base + E;     // [warps][stride]
     __shared__ uint32_t wsum[kRouteWarps];
     __shared__ uint32_t n_valid;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
-    for (int i = tid; i < kRouteWarps * E; i += kRouteThreads) hist[i] = 0u;
+    for (int i = tid; i < kRouteWarps * stride; i += kRouteThreads) hist[i] = 0u;
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int64_t per_warp = (((int64_t)n + ranks * kRouteThreads - 1) / (ranks * kRouteThreads)) * 32;
     const int64_t w0 = ((int64_t)rank * kRouteWarps + warp) * per_warp;
     const int f0 = (int)(w0 < n ? w0 : n);
     const int f1 = (int)(w0 + per_warp < n ? w0 + per_warp : n);
-    uint32_t* mine = hist + warp * E;
+    uint32_t* mine = hist + warp * stride;
     auto expert_of = [&](int f) {
         const int e = f < f1 ? __ldg(ids + f) : -1;
         return e >= 0 && e < E ? e : -1;
     };
-    for (int f = f0 + lane; f - lane < f1; f += 32) {
-        const int e = expert_of(f);
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    const int bits = 32 - __clz(E - 1);
+    auto count = [&](int e) {  // the id's rank in the run
+        uint32_t same = __ballot_sync(0xFFFFFFFFu, e >= 0);
+        for (int b = 0; b < bits; ++b) {
+            const uint32_t set = __ballot_sync(0xFFFFFFFFu, (e >> b) & 1);
+            same &= (e >> b) & 1 ? set : ~set;
+        }
+        const uint32_t before = e >= 0 ? mine[e] : 0;
         __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] = before + __popc(same);
+        __syncwarp();
+        return (int)(before + __popc(same & ((1u << lane) - 1u)));
+    };
+    int e_held[kHeldIds], r_held[kHeldIds];
+#pragma unroll
+    for (int i = 0; i < kHeldIds; ++i) e_held[i] = expert_of(f0 + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < kHeldIds; ++i)
+        if (f0 + 32 * i < f1) r_held[i] = count(e_held[i]);
+    for (int f = f0 + 32 * kHeldIds + lane; f - lane < f1; f += 32) {
+        const int r = count(expert_of(f));
+        if (f < f1) pos[f] = r;
     }
     __syncthreads();
-    if (tid < E) {  // counts -> prefixes over the CTA's warps
-        uint32_t sum = 0;
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const uint32_t c = hist[w * E + tid];
-            hist[w * E + tid] = sum;
-            sum += c;
+    for (int e = warp; e < E; e += kRouteWarps) {  // counts -> prefixes over the CTA's warps, a lane per warp
+        const uint32_t c = hist[lane * stride + e];
+        uint32_t inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
         }
-        total[tid] = sum;
+        hist[lane * stride + e] = inc - c;
+        if (lane == 31) total[e] = inc;
     }
-    cluster_sync();
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
     uint32_t all = 0, before = 0;
     if (tid < E) {
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const uint32_t c = ld_remote(total + tid, r);
-            if (r < rank) before += c;
-            all += c;
+        if (ranks == 1) {
+            all = total[tid];
+        } else {
+            uint32_t c[kRouteCluster];
+#pragma unroll
+            for (uint32_t r = 0; r < kRouteCluster; ++r) c[r] = ld_remote(total + tid, r);
+#pragma unroll
+            for (uint32_t r = 0; r < kRouteCluster; ++r) {
+                if (r < rank) before += c[r];
+                all += c[r];
+            }
         }
     }
     // inclusive scan of `all` over the experts
@@ -121,19 +154,17 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __re
         if (tid == E - 1) n_valid = inc;
     }
     __syncthreads();
-    for (int f = f0 + lane; f - lane < f1; f += 32) {
-        const int e = expert_of(f);
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        int p = -1;
-        if (e >= 0) p = (int)(base[e] + mine[e] + __popc(same & ((1u << lane) - 1u)));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-        if (f < f1) pos[f] = p;
+    auto place = [&](int f, int e, int r) {
+        if (f >= f1) return;
+        const int p = e >= 0 ? (int)(base[e] + mine[e]) + r : -1;
+        pos[f] = p;
         if (p >= 0) order[p] = f;
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeldIds; ++i) place(f0 + 32 * i + lane, e_held[i], r_held[i]);
+    for (int f = f0 + 32 * kHeldIds + lane; f - lane < f1; f += 32) place(f, expert_of(f), f < f1 ? pos[f] : 0);
     for (int64_t p = (int64_t)n_valid + rank * kRouteThreads + tid; p < n; p += ranks * kRouteThreads) order[p] = -1;
-    cluster_sync();  // a CTA's counts stay readable until every CTA has read them
+    if (ranks > 1) cluster_sync();  // a CTA's counts stay readable until every CTA has read them
 }
 
 // ---------------------------------------------------------------- rows
@@ -179,13 +210,41 @@ struct Row16<float> {
     __device__ static float rounded(float x) { return x; }
 };
 
-// Rows are worked on as 16-byte vectors, one thread per vector of a row (gather: of
-// kGatherRows rows), flat over the rows: neighbouring threads take neighbouring vectors,
-// a few rows fill as many threads as they can, and every thread has its rows' loads in
-// flight at once. The columns past the last whole vector go one by one to the thread
-// after it.
-constexpr int kGatherRows = 4;
+// Rows are worked on as vectors of 32 bytes (16 where rows are not 32-byte aligned), one
+// thread per vector of a row (gather: of kGatherRows rows), flat over the rows:
+// neighbouring threads take neighbouring vectors, a few rows fill as many threads as they
+// can, and every thread has its rows' loads in flight at once. The columns past the last
+// whole vector go one by one to the thread after it. 32768 x 2048 bf16 gathered from 8192
+// rows: 34.5 us with 16 bytes and four rows, 31.4 us with 32 bytes and two (25.6 us at the
+// copy bandwidth).
+constexpr int kGatherRows = 2;
 constexpr int kSlots = 4;  // slots whose rows are loaded together
+// CTAs per SM: few that stay suit the combination (8192 x 4 rows of 1536 bf16: 28 us with
+// 32, 24 us with 4), whose threads each hold four rows' loads
+constexpr int kCombineWaves = 4;
+
+template <int kBytes>
+struct Vec {
+    uint4 q[kBytes / 16];
+    __device__ __forceinline__ void load(const void* p) {
+        if constexpr (kBytes == 32)
+            asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y), "=r"(q[1].z),
+                  "=r"(q[1].w)
+                : "l"(p));
+        else
+            q[0] = __ldg(static_cast<const uint4*>(p));
+    }
+    // written once and not read here: kept from pushing the sources out of L2
+    __device__ __forceinline__ void store(void* p) const {
+        if constexpr (kBytes == 32)
+            asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(q[0].x), "r"(q[0].y),
+                         "r"(q[0].z), "r"(q[0].w), "r"(q[1].x), "r"(q[1].y), "r"(q[1].z), "r"(q[1].w)
+                         : "memory");
+        else
+            __stcs(static_cast<uint4*>(p), q[0]);
+    }
+};
 
 // This thread's (row, vector) with `per` vectors a row: a 64-bit division for the CTA's
 // first vector, the same in all its threads, and a 32-bit one for each thread.
@@ -197,12 +256,12 @@ __device__ __forceinline__ void split(int64_t first, uint32_t per, int64_t& row,
     v = i - r * per;
 }
 
-template <typename T>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T* __restrict__ X, int64_t n_tok, int64_t c,
                                                              int64_t ld, const int* __restrict__ order, int64_t k,
                                                              int64_t n_rows, T* __restrict__ Xs, int64_t ld_s) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int V = Row16<T>::kN;
+    constexpr int V = kBytes / sizeof(T);
     const uint32_t nv = (uint32_t)(c / V), per = (uint32_t)((c + V - 1) / V);
     const int64_t n = (n_rows + kGatherRows - 1) / kGatherRows * per;
     for (int64_t i = (int64_t)blockIdx.x * kRowThreads; i < n; i += (int64_t)gridDim.x * kRowThreads) {
@@ -218,13 +277,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T* __restrict
             if (t[r] >= n_tok) t[r] = -1;
         }
         if (v < nv) {
-            uint4 x[kGatherRows];
+            Vec<kBytes> x[kGatherRows];
 #pragma unroll
             for (int r = 0; r < kGatherRows; ++r)
-                if (t[r] >= 0) x[r] = __ldg(reinterpret_cast<const uint4*>(X + t[r] * ld) + v);
+                if (t[r] >= 0) x[r].load(X + t[r] * ld + v * V);
 #pragma unroll
             for (int r = 0; r < kGatherRows; ++r)
-                if (t[r] >= 0) reinterpret_cast<uint4*>(Xs + (p0 + r) * ld_s)[v] = x[r];
+                if (t[r] >= 0) x[r].store(Xs + (p0 + r) * ld_s + v * V);
         } else {
             for (int r = 0; r < kGatherRows; ++r)
                 if (t[r] >= 0)
@@ -234,13 +293,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const T* __restrict
 }
 
 // The sum runs over the slots in order, in FP32.
-template <typename T>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restrict__ Ys, int64_t n_rows, int64_t c,
                                                               int64_t ld_s, const int* __restrict__ pos,
                                                               const float* __restrict__ w, int64_t n_tok, int k,
                                                               T* __restrict__ Y, int64_t ld) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int V = Row16<T>::kN;
+    constexpr int V = kBytes / sizeof(T), P = Row16<T>::kN;
     const uint32_t nv = (uint32_t)(c / V), per = (uint32_t)((c + V - 1) / V);
     for (int64_t i = (int64_t)blockIdx.x * kRowThreads; i < n_tok * per; i += (int64_t)gridDim.x * kRowThreads) {
         int64_t t;
@@ -258,17 +317,20 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restric
                 ws[s] = p[s] >= 0 && w ? __ldg(w + t * k + s0 + s) : 1.0f;
             }
             if (v < nv) {
-                uint4 x[kSlots];
+                Vec<kBytes> x[kSlots];
 #pragma unroll
                 for (int s = 0; s < kSlots; ++s)
-                    if (p[s] >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(Ys + p[s] * ld_s) + v);
+                    if (p[s] >= 0) x[s].load(Ys + p[s] * ld_s + v * V);
 #pragma unroll
                 for (int s = 0; s < kSlots; ++s) {
                     if (p[s] < 0) continue;
-                    float f[V];
-                    Row16<T>::unpack(x[s], f);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = __fmaf_rn(ws[s], f[j], acc[j]);
+                    for (int h = 0; h < V / P; ++h) {
+                        float f[P];
+                        Row16<T>::unpack(x[s].q[h], f);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) acc[h * P + j] = __fmaf_rn(ws[s], f[j], acc[h * P + j]);
+                    }
                 }
             } else {
                 for (int s = 0; s < kSlots; ++s)
@@ -280,7 +342,15 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restric
         }
         T* dst = Y + t * ld;
         if (v < nv) {
-            reinterpret_cast<uint4*>(dst)[v] = Row16<T>::pack(acc);
+            Vec<kBytes> y;
+#pragma unroll
+            for (int h = 0; h < V / P; ++h) {
+                float f[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) f[j] = acc[h * P + j];
+                y.q[h] = Row16<T>::pack(f);
+            }
+            y.store(dst + v * V);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -291,9 +361,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* __restric
 
 // One CTA per token, kSlots slots at a time: dY[t] times each weight into the sorted
 // rows, and the dot products with the rows, in FP32 in an order fixed by the threads.
-constexpr int kGradThreads = 128;
+constexpr int kGradThreads = 64;
 
-template <typename T>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const T* __restrict__ dY, int64_t n_tok, int k,
                                                                     int64_t c, int64_t ld, const T* __restrict__ Ys,
                                                                     int64_t ld_s, int64_t n_rows,
@@ -301,7 +371,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const T* __r
                                                                     const float* __restrict__ w, T* __restrict__ dYs,
                                                                     int64_t ld_d, float* __restrict__ dw) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int V = Row16<T>::kN;
+    constexpr int V = kBytes / sizeof(T), P = Row16<T>::kN;
     __shared__ float part[kGradThreads / 32][kSlots];
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t nv = c / V;
@@ -317,30 +387,38 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const T* __r
                 ws[s] = p[s] >= 0 && w ? __ldg(w + t * k + s0 + s) : 1.0f;
             }
             for (int64_t v = tid; v < nv; v += kGradThreads) {
-                uint4 x[kSlots];
-                const uint4 gv = __ldg(reinterpret_cast<const uint4*>(dy) + v);
+                Vec<kBytes> x[kSlots], gv;
+                gv.load(dy + v * V);
                 if (dw) {
 #pragma unroll
                     for (int s = 0; s < kSlots; ++s)
-                        if (p[s] >= 0) x[s] = __ldg(reinterpret_cast<const uint4*>(Ys + p[s] * ld_s) + v);
+                        if (p[s] >= 0) x[s].load(Ys + p[s] * ld_s + v * V);
                 }
                 float g[V];
-                Row16<T>::unpack(gv, g);
+#pragma unroll
+                for (int h = 0; h < V / P; ++h) {
+                    float f[P];
+                    Row16<T>::unpack(gv.q[h], f);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) g[h * P + j] = f[j];
+                }
 #pragma unroll
                 for (int s = 0; s < kSlots; ++s) {
                     if (p[s] < 0) continue;
-                    if (dw) {
-                        float y[V];
-                        Row16<T>::unpack(x[s], y);
+                    Vec<kBytes> out;
 #pragma unroll
-                        for (int j = 0; j < V; ++j) dot[s] = __fmaf_rn(g[j], y[j], dot[s]);
-                    }
-                    if (dYs) {
-                        float d[V];
+                    for (int h = 0; h < V / P; ++h) {
+                        float y[P], d[P];
+                        if (dw) {
+                            Row16<T>::unpack(x[s].q[h], y);
 #pragma unroll
-                        for (int j = 0; j < V; ++j) d[j] = g[j] * ws[s];
-                        reinterpret_cast<uint4*>(dYs + p[s] * ld_d)[v] = Row16<T>::pack(d);
+                            for (int j = 0; j < P; ++j) dot[s] = __fmaf_rn(g[h * P + j], y[j], dot[s]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < P; ++j) d[j] = g[h * P + j] * ws[s];
+                        out.q[h] = Row16<T>::pack(d);
                     }
+                    if (dYs) out.store(dYs + p[s] * ld_d + v * V);
                 }
             }
             for (int64_t j = nv * V + tid; j < c; j += kGradThreads) {
@@ -385,6 +463,11 @@ lh_status check_rows(const char* name, const void* p, lh_dtype t, int64_t c, int
     return LH_OK;
 }
 
+// Whether the rows of p are 32-byte aligned.
+bool wide_rows(const void* p, lh_dtype t, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (ld * elem_bytes(t)) % 32 == 0;
+}
+
 lh_status check_slots(int64_t n_tok, int64_t k) {
     if (n_tok < 0 || k < 1) return fail(LH_ERR_INVALID_ARG, "n_tok must be >= 0 and k >= 1");
     if (k > INT_MAX || (n_tok > 0 && n_tok > INT_MAX / k))
@@ -425,12 +508,12 @@ extern "C" lh_status lh_route_tokens(const int32_t* ids, int64_t n_tok, int64_t 
         return fail(LH_ERR_INVALID_ARG, "order, pos and ids must be different arrays");
     if (sm_count() <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     const int n = (int)(n_tok * k), E = (int)n_experts;
-    const size_t smem = (size_t)(kRouteWarps + 2) * E * sizeof(uint32_t);
+    const size_t smem = ((size_t)kRouteWarps * (E | 1) + 2 * (size_t)E) * sizeof(uint32_t);
     static std::atomic<uint64_t> done{0};  // for the largest number of experts
-    s = allow_shared((const void*)route_kernel, (size_t)(kRouteWarps + 2) * kMaxExperts * sizeof(uint32_t), done);
+    s = allow_shared((const void*)route_kernel, (size_t)(kRouteWarps + 2) * (kMaxExperts + 1) * sizeof(uint32_t), done);
     if (s != LH_OK) return s;
-    // one CTA walks 4096 ids in 4 steps of its warps; more ids want the cluster's eight SMs
-    const unsigned ctas = n <= 4 * kRouteThreads ? 1 : kRouteCluster;
+    // one step of one CTA takes 1024 ids; more want the eight SMs of a cluster (4096 ids: 6.7 us in one CTA, 5.0 us)
+    const unsigned ctas = n <= kRouteThreads ? 1 : kRouteCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kRouteThreads);
@@ -464,15 +547,17 @@ extern "C" lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_t
     if (n_tok == 0 || c == 0 || n_rows == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const int64_t per = (c * elem_bytes(dtype) + 15) / 16;
+    const bool wide = wide_rows(X, dtype, ld_x) && wide_rows(Xs, dtype, ld_xs);
+    const int bytes = wide ? 32 : 16;
+    const int64_t per = (c * elem_bytes(dtype) + bytes - 1) / bytes;
     const unsigned grid = grid_for((n_rows + kGatherRows - 1) / kGatherRows * per, kRowThreads, sms, 32);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int* o = (const int*)order;
     if (dtype == LH_BF16)
-        return launch_rows("gather_kernel launch", gather_kernel<uint16_t>, grid, kRowThreads, st, (const uint16_t*)X, n_tok, c, ld_x,
-                           o, k, n_rows, (uint16_t*)Xs, ld_xs);
-    return launch_rows("gather_kernel launch", gather_kernel<float>, grid, kRowThreads, st, (const float*)X, n_tok, c, ld_x, o, k,
-                       n_rows, (float*)Xs, ld_xs);
+        return launch_rows("gather_kernel launch", wide ? gather_kernel<uint16_t, 32> : gather_kernel<uint16_t, 16>, grid,
+                           kRowThreads, st, (const uint16_t*)X, n_tok, c, ld_x, o, k, n_rows, (uint16_t*)Xs, ld_xs);
+    return launch_rows("gather_kernel launch", wide ? gather_kernel<float, 32> : gather_kernel<float, 16>, grid,
+                       kRowThreads, st, (const float*)X, n_tok, c, ld_x, o, k, n_rows, (float*)Xs, ld_xs);
 }
 
 extern "C" lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n_rows, int64_t c, int64_t ld_ys,
@@ -492,13 +577,17 @@ extern "C" lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n
     if (n_tok == 0 || c == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const unsigned grid = grid_for(n_tok * ((c * elem_bytes(dtype) + 15) / 16), kRowThreads, sms, 32);
+    const bool wide = wide_rows(Ys, dtype, ld_ys) && wide_rows(Y, dtype, ld_y);
+    const int bytes = wide ? 32 : 16;
+    const unsigned grid = grid_for(n_tok * ((c * elem_bytes(dtype) + bytes - 1) / bytes), kRowThreads, sms, kCombineWaves);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == LH_BF16)
-        return launch_rows("combine_kernel launch", combine_kernel<uint16_t>, grid, kRowThreads, st, (const uint16_t*)Ys, n_rows, c,
-                           ld_ys, (const int*)pos, weights, n_tok, (int)k, (uint16_t*)Y, ld_y);
-    return launch_rows("combine_kernel launch", combine_kernel<float>, grid, kRowThreads, st, (const float*)Ys, n_rows, c, ld_ys,
-                       (const int*)pos, weights, n_tok, (int)k, (float*)Y, ld_y);
+        return launch_rows("combine_kernel launch", wide ? combine_kernel<uint16_t, 32> : combine_kernel<uint16_t, 16>,
+                           grid, kRowThreads, st, (const uint16_t*)Ys, n_rows, c, ld_ys, (const int*)pos, weights, n_tok,
+                           (int)k, (uint16_t*)Y, ld_y);
+    return launch_rows("combine_kernel launch", wide ? combine_kernel<float, 32> : combine_kernel<float, 16>, grid,
+                       kRowThreads, st, (const float*)Ys, n_rows, c, ld_ys, (const int*)pos, weights, n_tok, (int)k,
+                       (float*)Y, ld_y);
 }
 
 extern "C" lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int64_t n_tok, int64_t k, int64_t c,
@@ -522,13 +611,17 @@ extern "C" lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int6
     if (n_tok == 0 || (c == 0 && !dweights)) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
-    const unsigned grid = grid_for(n_tok, 1, sms, 64);
+    const bool wide = wide_rows(dY, dtype, ld_dy) && (!dweights || wide_rows(Ys, dtype, ld_ys)) &&
+                      (!dYs || wide_rows(dYs, dtype, ld_dys));
+    const unsigned grid = grid_for(n_tok, 1, sms, 8);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == LH_BF16)
-        return launch_rows("combine_grad_kernel launch", combine_grad_kernel<uint16_t>, grid, kGradThreads, st, (const uint16_t*)dY,
-                           n_tok, (int)k, c, ld_dy, (const uint16_t*)Ys, ld_ys, n_rows, (const int*)pos, weights,
-                           (uint16_t*)dYs, ld_dys, dweights);
-    return launch_rows("combine_grad_kernel launch", combine_grad_kernel<float>, grid, kGradThreads, st, (const float*)dY, n_tok,
-                       (int)k, c, ld_dy, (const float*)Ys, ld_ys, n_rows, (const int*)pos, weights, (float*)dYs, ld_dys,
-                       dweights);
+        return launch_rows("combine_grad_kernel launch",
+                           wide ? combine_grad_kernel<uint16_t, 32> : combine_grad_kernel<uint16_t, 16>, grid,
+                           kGradThreads, st, (const uint16_t*)dY, n_tok, (int)k, c, ld_dy, (const uint16_t*)Ys, ld_ys,
+                           n_rows, (const int*)pos, weights, (uint16_t*)dYs, ld_dys, dweights);
+    return launch_rows("combine_grad_kernel launch",
+                       wide ? combine_grad_kernel<float, 32> : combine_grad_kernel<float, 16>, grid, kGradThreads, st,
+                       (const float*)dY, n_tok, (int)k, c, ld_dy, (const float*)Ys, ld_ys, n_rows, (const int*)pos, weights,
+                       (float*)dYs, ld_dys, dweights);
 }
