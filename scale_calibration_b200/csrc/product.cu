@@ -14,12 +14,15 @@
 // rows that a ragged group's last tile needs.
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
 #include "scale_tiles.cuh"
 #include "tcgen05.cuh"
+#include "token_block.cuh"
+#include "tokens.cuh"
 
 namespace lh {
 namespace {
@@ -46,6 +49,11 @@ struct ProdArgs {
     const float* xg;         // [n_rows]
     const float* wg;         // [G]
     void* Y;
+    const void* X;           // the tokens themselves (from_tokens), [n_rows][ld_x], and their given amax or null
+    int64_t ld_x;
+    const float* gamax;
+    int J;
+    bool wide_x;
     bool early;              // the kernel before leaves weights, scales and offsets alone: no need to wait for those
 };
 
@@ -63,7 +71,11 @@ struct Shape {
     static_assert(kStages * kStageBytes >= 2 * kT * kM * 4, "split: the partial sums reuse the ring");
 };
 
+constexpr int kFewTokens = 8;  // most tokens that the product quantises itself
+
 struct Control {
+    uint32_t amax[4][kFewTokens];  // of the tokens, by warp
+    float gscale[kFewTokens];
     uint64_t full[Shape::kStages], empty[Shape::kStages], tfull[2], tempty[2], done, sums;
     uint32_t tmem;
     int abort_flag;
@@ -240,16 +252,79 @@ struct Part<__nv_bfloat16> {
     }
 };
 
+// The tokens of a fused product (at most kFewTokens, by four warps): their global scales,
+// and the stages ks0 .. ks1 of their codes, in the 128-byte swizzle that the products read
+// (the 16-byte pieces of a row swapped by the row's number), with the scale tiles.
+template <typename Tin>
+__device__ void write_tokens(const ProdArgs& p, Control& C, uint32_t ring, int ks0, int ks1, volatile int* abort_flag) {
+    using S = Shape;
+    const int th = threadIdx.x - 64, warp = th >> 5, lane = th & 31;
+    const int n = (int)p.n_rows;
+    const Tin* X = static_cast<const Tin*>(p.X);
+    Held<Tin> h;
+    for (int r = 0; r < n; ++r) {
+        uint32_t m = 0;
+        for (int j = th; j < p.J; j += 128) {
+            h.load(X + r * p.ld_x + 16 * (int64_t)j, p.wide_x);
+            m = max(m, h.max_bits());
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0) C.amax[warp][r] = m;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const int r = th >> 4, jj = th & 15;  // a thread per block of a stage
+    const bool mine = r < n;
+    uint32_t m = 0;
+    if (mine) m = max(max(C.amax[0][r], C.amax[1][r]), max(C.amax[2][r], C.amax[3][r]));
+    const bool bad = m >= 0x7F800000u;
+    const RowScale rs(p.gamax ? __ldg(p.gamax) : __uint_as_float(m));
+    if (mine && jj == 0) C.gscale[r] = bad ? rs.nan : rs.g;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int ks = ks0; ks < ks1; ++ks) {
+        const int j = 16 * ks + jj;
+        uint32_t code = 0, word[2] = {0u, 0u};
+        if (mine && j < p.J) {  // blocks past c_in: zeros
+            float o[16];
+            h.load(X + r * p.ld_x + 16 * (int64_t)j, p.wide_x);
+            code = quantize_held<false, true>(h, h.max_bits(), rs, bad && !p.gamax, o, word);
+        }
+        if (!warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag)) {
+            give_up(abort_flag);
+            break;
+        }
+        if (mine) {
+            const uint32_t b = ring + stage * S::kStageBytes + S::kA, sb = b + S::kB + S::kSa;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(b + r * kRowBytes + ((((jj >> 1) ^ r) & 7) << 4) + (jj & 1) * 8),
+                         "r"(word[0]), "r"(word[1])
+                         : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sb + (jj >> 2) * kTileBytes + r * 16 + (jj & 3)), "r"(code) : "memory");
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&C.full[stage]));
+        if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the scales are there for all
+}
+
 // kSplit: a cluster of CTAs works on one tile, each on a part of c_in; the partial sums
 // meet in distributed shared memory, each CTA adding up those of its share of the tokens in the
 // order of the parts (the same sums every time). Without it a CTA walks over whole tiles.
-template <bool kSplit, typename Tout>
+//
+// Tin: with few tokens of type Tin instead of quantised ones (kSplit only), every CTA
+// quantises its part of them: the epilogue warps, idle until the sums are ready, take each
+// token's largest |x| and write the codes and scales of a stage where TMA would put them,
+// while the weights are on their way, in one launch instead of two.
+template <bool kSplit, typename Tout, typename Tin = void>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
                                                               const __grid_constant__ CUtensorMap wsmap,
                                                               const __grid_constant__ CUtensorMap xsmap,
                                                               const ProdArgs p) {
     using S = Shape;
+    constexpr bool kFused = !std::is_void_v<Tin>;
+    static_assert(kSplit || !kFused, "few tokens make few tiles");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
@@ -263,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(smem_u32(&C.full[s]), 1);
+            mbar_init(smem_u32(&C.full[s]), kFused ? 5 : 1);  // TMA, and the warps that quantise
             mbar_init(smem_u32(&C.empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -295,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int wsrow = (int)((t.g * p.mtiles + t.mt) * p.steps);
             const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
             const int boxes = (t.rows + kBox - 1) / kBox;
-            const uint32_t bytes = S::kA + boxes * kBox * kRowBytes + S::kSa + S::kSb;
+            const uint32_t bytes = S::kA + S::kSa + (kFused ? 0 : boxes * kBox * kRowBytes + S::kSb);
             auto weights = [&](int s, int ks) {
                 const uint32_t bar = smem_u32(&C.full[s]), a = ring + s * S::kStageBytes;
                 mbar_expect_tx(bar, bytes);
@@ -316,9 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 if (elect_one()) {
                     const uint32_t bar = smem_u32(&C.full[stage]), b = ring + stage * S::kStageBytes + S::kA;
                     if (ahead == 0) weights(stage, ks);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(b + i * kBox * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * kBox, bar);
-                    tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
+                    if constexpr (!kFused) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(b + i * kBox * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * kBox, bar);
+                        tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
+                    }
                 }
                 __syncwarp();
                 if (ahead > 0) --ahead;
@@ -407,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (!ok) give_up(abort_flag);
     } else {
         if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if constexpr (kFused) write_tokens<Tin>(p, C, ring, ks0, ks1, abort_flag);
         if (walk.find(p, first, t) && !warp_wait(smem_u32(&C.tfull[0]), 0, abort_flag)) give_up(abort_flag);
     }
     if constexpr (kSplit) {
@@ -426,7 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const float gw = __ldg(p.wg + t.g);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (32 * j + lane < tokens_of(rank)) gx[j] = gw * __ldg(p.xg + row0 + 32 * j + lane);
+                if (32 * j + lane < tokens_of(rank)) {
+                    if constexpr (kFused) gx[j] = gw * C.gscale[rank * per + 32 * j + lane];
+                    else gx[j] = gw * __ldg(p.xg + row0 + 32 * j + lane);
+                }
             fence_after();
             for (int c = 0; c < t.rows; c += 32) {
                 uint32_t r[32];
@@ -449,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                                           tokens_of(r) * kM * 4, cluster_addr(bar, r));
             }
             __syncwarp();
-            if (got) {
-                if (!warp_wait(bar, 0, abort_flag)) give_up(abort_flag);
+            if (got && !warp_wait(bar, 0, abort_flag)) give_up(abort_flag);
+            if (tokens_of(rank) > 0) {
                 const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
                 Tout* y = static_cast<Tout*>(p.Y) + row0 * p.ld_y + ch;
                 const int n = tokens_of(rank);
@@ -701,22 +782,24 @@ bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kSplit, typename Tout>
+template <bool kSplit, typename Tout, typename Tin = void>
 lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                          const ProdArgs& p, int parts, int sms, cudaStream_t st) {
     using S = Shape;
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512) return fail(LH_ERR_UNSUPPORTED, "too many scale tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
-    if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox) ||
-        !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
-        return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    bool ok = make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) && make_scale_map(encode, &wsmap, p.ws, ws_tiles);
+    if constexpr (std::is_void_v<Tin>)
+        ok = ok && make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox) && make_scale_map(encode, &xsmap, p.xs, xs_tiles);
+    else
+        xmap = wmap, xsmap = wsmap;  // not used
+    if (!ok) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const int64_t tiles = (p.offsets ? p.n_rows / kT + p.G : (p.n_rows + kT - 1) / kT) * p.mtiles;  // at most
     if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
     constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 4 * kTurnBytes + 1024 + sizeof(Control);
     static_assert(smem <= 227 * 1024, "shared memory");
-    auto kernel = product_kernel<kSplit, Tout>;
+    auto kernel = product_kernel<kSplit, Tout, Tin>;
     static std::atomic<uint64_t> done{0};
     lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
@@ -772,6 +855,16 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_pair_kernel launch");
 }
 
+// Parts of c_in for the tiles of one matrix and at most 128 tokens: as many as SMs allow, in
+// cluster sizes that pack the GPCs (1 x 17408 -> 5120, 40 tiles: 21.2 us in two parts, 18.4 us
+// in three).
+int split_parts(const ProdArgs& p, int sms) {
+    const int most = p.mtiles > 0 ? sms / p.mtiles : 1;
+    for (const int parts : {8, 6, 4, 3, 2})
+        if (parts <= most && parts <= p.stages_k) return parts;
+    return 1;
+}
+
 // Which kernel. One matrix: CTA pairs above 128 tokens (160 x 4096 -> 12288: 13.1 us
 // against 16.1 us in two tiles of single CTAs; 128: 11.2 us single, 13.0 us in pairs), else
 // single CTAs, with c_in split over clusters while the tiles leave half of the SMs idle.
@@ -784,8 +877,7 @@ lh_status dispatch(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, c
     if (p.offsets ? p.n_rows >= kPairRows * p.G : p.n_rows > kT)
         return launch_pair<Tout>(encode, X, W, c_in, p, sms, st);
     if (!p.offsets) {
-        int parts = 1;
-        while (parts < 8 && p.mtiles * parts * 2 <= sms && parts * 2 <= p.stages_k) parts *= 2;
+        const int parts = split_parts(p, sms);
         if (parts > 1) return launch_product<true, Tout>(encode, X, W, c_in, p, parts, sms, st);
     }
     return launch_product<false, Tout>(encode, X, W, c_in, p, 1, sms, st);
@@ -815,6 +907,18 @@ lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const 
 
 namespace lh {
 namespace {
+ProdArgs product_args(const uint8_t* X_scales, const float* X_gscale, const uint8_t* W_scales, const float* W_gscale,
+                      const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out, int64_t c_in, void* Y,
+                      int64_t ld_y, bool early) {
+    ProdArgs p = {};
+    p.offsets = offsets; p.G = n_groups; p.n_rows = n_rows; p.c_out = c_out; p.ld_y = ld_y;
+    p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
+    p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
+    p.steps = (int)scale_steps(c_in);
+    p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y; p.early = early;
+    return p;
+}
+
 lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale, const uint8_t* W_packed,
                  const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets, int64_t n_groups,
                  int64_t n_rows, int64_t c_out, int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, bool early,
@@ -833,15 +937,36 @@ lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* 
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     auto encode = encode_fn();
     if (!encode) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-    ProdArgs p;
-    p.offsets = offsets; p.G = n_groups; p.n_rows = n_rows; p.c_out = c_out; p.ld_y = ld_y;
-    p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
-    p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
-    p.steps = (int)scale_steps(c_in);
-    p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y; p.early = early;
+    const ProdArgs p = product_args(X_scales, X_gscale, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y,
+                                    ld_y, early);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (out_dtype == LH_BF16) return dispatch<__nv_bfloat16>(encode, X_packed, W_packed, c_in, p, sms, st);
     return dispatch<float>(encode, X_packed, W_packed, c_in, p, sms, st);
+}
+
+// Whether the product takes the tokens themselves: one matrix in few tiles, and so little of
+// them that every CTA can look at it all. From the tokens on, 1 x 4096 -> 4096 takes 7.3 us so
+// and 7.4 us in two launches, with 2.3 us less of the host's time; 2 tokens take 7.9 and
+// 7.5 us, 1 x 17408 -> 5120 24.8 and 21.2 us.
+bool can_fuse(const ProdArgs& p, int64_t c_in, const int32_t* rows, int sms) {
+    return !rows && !p.offsets && p.n_rows <= kFewTokens && p.n_rows * c_in <= 4096 && split_parts(p, sms) > 1;
+}
+
+// The product of few tokens, from the tokens on. Arguments as lh_nvfp4_linear has checked them.
+lh_status fused(ProdArgs p, const void* X, lh_dtype x_dtype, int64_t c_in, int64_t ld_x, const float* gamax,
+                const uint8_t* W_packed, lh_dtype out_dtype, int sms, cudaStream_t st) {
+    auto encode = encode_fn();
+    if (!encode) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    p.X = X; p.ld_x = ld_x; p.gamax = gamax; p.J = (int)(c_in / 16);
+    p.wide_x = (reinterpret_cast<uintptr_t>(X) & 31) == 0 && (ld_x * elem_bytes(x_dtype)) % 32 == 0;
+    const int parts = split_parts(p, sms);
+    if (x_dtype == LH_BF16)
+        return out_dtype == LH_BF16
+                   ? launch_product<true, __nv_bfloat16, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, sms, st)
+                   : launch_product<true, float, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, sms, st);
+    return out_dtype == LH_BF16
+               ? launch_product<true, __nv_bfloat16, float>(encode, nullptr, W_packed, c_in, p, parts, sms, st)
+               : launch_product<true, float, float>(encode, nullptr, W_packed, c_in, p, parts, sms, st);
 }
 
 }  // namespace
@@ -900,6 +1025,16 @@ extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_
     uint8_t* packed = ws + w.packed;
     uint8_t* scales = ws + w.scales;
     float* gscale = reinterpret_cast<float*>(ws + w.gscale);
+    s = check_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, packed, scales, gscale,
+                     nullptr, LH_F32);
+    if (s != LH_OK) return s;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    const ProdArgs few = product_args(nullptr, nullptr, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y,
+                                      ld_y, false);
+    if (can_fuse(few, c_in, rows, sms))
+        return fused(few, X, x_dtype, c_in, ld_x, global_amax, W_packed, out_dtype, sms,
+                     reinterpret_cast<cudaStream_t>(stream));
     s = lh_quantize_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, global_amax, packed,
                            scales, gscale, nullptr, LH_F32, stream);
     if (s != LH_OK) return s;

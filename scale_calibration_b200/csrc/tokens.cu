@@ -9,8 +9,9 @@
 // as lh_baseline_scales and lh_quantize_nvfp4 do for a matrix, in one pass over X.
 #include <climits>
 
-#include "nvfp4_block.cuh"
 #include "scale_tiles.cuh"
+#include "token_block.cuh"
+#include "tokens.cuh"
 
 namespace lh {
 namespace {
@@ -53,56 +54,6 @@ __device__ __forceinline__ bool find_group(const TokenArgs& p, int row, int& g, 
     return lo <= row && row < __ldg(p.offsets + g + 1);
 }
 
-// 16 values as they lie in memory.
-template <typename T>
-struct Held {
-    uint32_t v[8 * (sizeof(T) / 2)];
-    // wide: p is 32-byte aligned. A warp's 32-byte accesses fill whole sectors, where 16
-    // bytes of every 32 or 64 make L2 handle each sector twice.
-    __device__ void load(const T* p, bool wide) {
-        if (wide) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-                uint32_t* u = v + 8 * i;
-                asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                    : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                    : "l"(reinterpret_cast<const uint32_t*>(p) + 8 * i));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
-            }
-        }
-    }
-    __device__ void floats(float (&w)[16]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (sizeof(T) == 2) {
-                w[2 * i] = __uint_as_float(v[i] << 16);
-                w[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-            } else {
-                w[2 * i] = __uint_as_float(v[2 * i]);
-                w[2 * i + 1] = __uint_as_float(v[2 * i + 1]);
-            }
-        }
-    }
-    // Bits of the largest |x|; as integers, infinities and NaN come out on top.
-    __device__ uint32_t max_bits() const {
-        uint32_t m = 0;
-        if constexpr (sizeof(T) == 2) {  // two bf16 at a time
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
-            return max(m << 16, m & 0xFFFF0000u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m = max(m, v[i] & 0x7FFFFFFFu);
-            return m;
-        }
-    }
-};
-
 __device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
                  "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
@@ -128,51 +79,6 @@ __device__ __forceinline__ void store16(float* p, const float (&o)[16], bool wid
         store32(p + 8 * i, u);
     }
 }
-
-// A row's global scale, with its reciprocal where the quotient of a block needs no
-// division: with g in [2^-85, 2^100], q = RN(a y) and RN(q + (a - q g) y) with y = RN(1/g)
-// is the correctly rounded a / g for |a| >= 2^-100 (P. Markstein, IBM J. Res. Dev. 34(1),
-// 1990: the residual is exact), and a smaller a gives less than 2^-14 either way, code 1.
-// The same holds for a / 6, and for g itself.
-struct RowScale {
-    float g, ny, nan;
-    bool fast;
-    // From an amax >= 0 (or NaN).
-    __device__ explicit RowScale(float amax) {
-        nan = __int_as_float(0x7FFFFFFF);
-        fast = amax >= 6.948286e-23f && amax <= 3.3230700e33f;  // 2688 * [2^-85, 2^100], rounded inwards
-        if (fast) {
-            g = quotient(amax, 2688.0f, -1.0f / 2688.0f);
-            ny = -__frcp_rn(g);
-        } else {
-            g = __fdiv_rn(amax, 2688.0f);
-            ny = 0.0f;
-        }
-    }
-    __device__ static float quotient(float a, float d, float nyd) {
-        const float nq = __fmul_rn(a, nyd);          // -q
-        const float r = __fmaf_rn(nq, d, a);         // a - q d
-        return -__fmaf_rn(r, nyd, nq);
-    }
-    // E4M3 code of a block whose largest |x| is a, and the block's scale.
-    // kGiven: a may be above the row's amax.
-    template <bool kGiven>
-    __device__ uint32_t code(float a, float& s) const {
-        uint32_t c = 1;
-        if (fast)
-            {
-            const float sixth = quotient(a, 6.0f, -1.0f / 6.0f);
-            c = (uint32_t)e4m3_rne_code(quotient(kGiven ? fminf(sixth, 512.0f * g) : sixth, g, ny));  // above: the largest code
-        }
-        else if (g != 0.0f)
-            c = (uint32_t)e4m3_rne_code(__fdiv_rn(__fdiv_rn(a, 6.0f), g));
-        c = c < 1 ? 1 : c;
-        uint32_t h2;  // the code's value, exact in f16
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
-        s = __fmul_rn(__low2float(*reinterpret_cast<const __half2*>(&h2)), g);
-        return c;
-    }
-};
 
 // kWarps warps per row. With the token's own scale each thread loads its blocks of the
 // row and keeps them, the warps agree on the row's largest |x|, and the blocks are
@@ -251,24 +157,9 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
                 if (j - lane >= 4 * p.steps) break;  // the same for the warp
                 uint32_t code = 0;
                 if (j < J) {
-                    float s;
-                    code = rs.template code<kGiven>(__uint_as_float(bb[i]), s);
-                    if (bb[i] >= 0x7F800000u || bad_token) {
-                        code = 0x7F;
-                        s = rs.nan;
-                    }
-                    float w[16], o[16];
+                    float o[16];
                     uint32_t word[2];
-                    h[i].floats(w);
-                    if constexpr (kGiven) {
-                        // far above the amax, the quotients of quantize_block would overflow
-                        const float far = 1.1529215e18f * s;
-                        if (s >= 2.524355e-29f && __uint_as_float(bb[i]) > far) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = fminf(fmaxf(w[e], -far), far);
-                        }
-                    }
-                    quantize_block<kOut, true>(w, s, o, word);
+                    code = quantize_held<kOut, kGiven>(h[i], bb[i], rs, bad_token, o, word);
                     reinterpret_cast<uint2*>(p.packed)[out0 + j] = make_uint2(word[0], word[1]);
                     if constexpr (kOut) store16(out + (out0 + j) * 16, o, p.wide_out);
                 }
@@ -354,6 +245,33 @@ lh_status launch_tokens(const void* X, const TokenArgs& p, void* out, lh_dtype o
 }
 
 }  // namespace
+
+lh_status check_tokens(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c_in, int64_t ld_x, const int32_t* rows,
+                       int64_t row_div, int64_t n_rows, const int64_t* offsets, int64_t n_groups, const uint8_t* packed,
+                       const uint8_t* scale_tiles, const float* token_scale, const void* X_out, lh_dtype out_dtype) {
+    if (!valid_dtype(x_dtype) || (X_out && !valid_dtype(out_dtype))) return fail(LH_ERR_UNSUPPORTED, "unknown dtype");
+    if (!X || !packed || !scale_tiles || !token_scale) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_src < 0 || n_rows < 0 || c_in < 0 || n_groups < 1)
+        return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
+    if (row_div < 1) return fail(LH_ERR_INVALID_ARG, "row_div must be >= 1");
+    if (n_rows > INT_MAX - 512 || n_groups > INT_MAX - 512)
+        return fail(LH_ERR_UNSUPPORTED, "n_rows and n_groups must be below 2^31 - 512");
+    if (row_div > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "row_div must be below 2^31");
+    if (!rows && (row_div != 1 || n_rows > n_src))
+        return fail(LH_ERR_INVALID_ARG, "without rows, row_div must be 1 and n_rows at most n_src");
+    if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
+    if (c_in % 16 != 0) return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a multiple of 16", (long long)c_in);
+    if (ld_x < c_in) return fail(LH_ERR_INVALID_ARG, "ld_x=%lld < c_in=%lld", (long long)ld_x, (long long)c_in);
+    if (!aligned16(X) || (ld_x * elem_bytes(x_dtype)) % 16 != 0)
+        return fail(LH_ERR_ALIGNMENT, "X must be 16-byte aligned with 16-byte aligned rows");
+    if (!aligned16(packed) || !aligned16(scale_tiles) || !aligned16(X_out))
+        return fail(LH_ERR_ALIGNMENT, "packed, scale_tiles and X_out must be 16-byte aligned");
+    if (c_in > INT_MAX - 64) return fail(LH_ERR_UNSUPPORTED, "c_in must be below 2^31 - 64");
+    if (X == X_out || X == (const void*)packed || X == (const void*)scale_tiles || packed == scale_tiles)
+        return fail(LH_ERR_INVALID_ARG, "outputs must not alias X or one another");
+    return LH_OK;
+}
+
 }  // namespace lh
 
 extern "C" size_t lh_nvfp4_token_scale_bytes(int64_t n_rows, int64_t c_in, int64_t n_groups) {
@@ -396,26 +314,9 @@ extern "C" lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t
                                         void* stream) {
     using namespace lh;
     clear_error();
-    if (!valid_dtype(x_dtype) || (X_out && !valid_dtype(out_dtype))) return fail(LH_ERR_UNSUPPORTED, "unknown dtype");
-    if (!X || !packed || !scale_tiles || !token_scale) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
-    if (n_src < 0 || n_rows < 0 || c_in < 0 || n_groups < 1)
-        return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
-    if (row_div < 1) return fail(LH_ERR_INVALID_ARG, "row_div must be >= 1");
-    if (n_rows > INT_MAX - 512 || n_groups > INT_MAX - 512)
-        return fail(LH_ERR_UNSUPPORTED, "n_rows and n_groups must be below 2^31 - 512");
-    if (row_div > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "row_div must be below 2^31");
-    if (!rows && (row_div != 1 || n_rows > n_src))
-        return fail(LH_ERR_INVALID_ARG, "without rows, row_div must be 1 and n_rows at most n_src");
-    if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
-    if (c_in % 16 != 0) return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a multiple of 16", (long long)c_in);
-    if (ld_x < c_in) return fail(LH_ERR_INVALID_ARG, "ld_x=%lld < c_in=%lld", (long long)ld_x, (long long)c_in);
-    if (!aligned16(X) || (ld_x * elem_bytes(x_dtype)) % 16 != 0)
-        return fail(LH_ERR_ALIGNMENT, "X must be 16-byte aligned with 16-byte aligned rows");
-    if (!aligned16(packed) || !aligned16(scale_tiles) || !aligned16(X_out))
-        return fail(LH_ERR_ALIGNMENT, "packed, scale_tiles and X_out must be 16-byte aligned");
-    if (c_in > INT_MAX - 64) return fail(LH_ERR_UNSUPPORTED, "c_in must be below 2^31 - 64");
-    if (X == X_out || X == (const void*)packed || X == (const void*)scale_tiles || packed == scale_tiles)
-        return fail(LH_ERR_INVALID_ARG, "outputs must not alias X or one another");
+    const lh_status ok = check_tokens(X, x_dtype, n_src, c_in, ld_x, rows, row_div, n_rows, offsets, n_groups, packed,
+                                      scale_tiles, token_scale, X_out, out_dtype);
+    if (ok != LH_OK) return ok;
     if (n_rows == 0 || c_in == 0 || n_src == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");

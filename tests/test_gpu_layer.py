@@ -514,6 +514,33 @@ def test_linear_from_the_tokens(cuda_ok, n, m, c, tensor, t):
     assert (y[:, m:] == 4.0).all()
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("given", [None, 3.0, 1e-30, 0.0])
+@pytest.mark.parametrize("n,m,c", [(1, 100, 32), (1, 4096, 4096), (2, 700, 1056), (3, 130, 9248), (5, 64, 480),
+                                   (8, 19000, 64), (8, 1536, 512), (8, 9000, 480), (7, 128, 4384),
+                                   (4, 300, 1024), (1, 12288, 4096), (1, 257, 17408)])
+def test_linear_of_few_tokens_equals_its_two_calls(cuda_ok, n, m, c, given, t):
+    lh = _lh()
+    rng = np.random.default_rng(n + m + c)
+    w, _, _ = bank(rng, 1, m, c)
+    buf = torch.full((n, c + 8), 9.0, dtype=DT[t], device="cuda")
+    x = buf[:, :c]
+    x.copy_(torch.from_numpy((rng.standard_normal((n, c)) * np.exp(rng.standard_normal(c))).astype(np.float32)))
+    if n > 2:
+        x[0] = 0
+        x[1, c // 3] = float("nan")
+        x[2, c - 1] = -float("inf")
+    amax = None if given is None else torch.tensor([given], device="cuda")
+    y = torch.full((n, pitch(m, t)), 4.0, dtype=DT[t], device="cuda")
+    linear(x, n, c, w, m, y, amax=amax)
+    packed, tiles, g, _ = quantize(x, n, c, amax=amax)
+    y2 = torch.full_like(y, 4.0)
+    matmul(packed, tiles, g, *w, None, y2, m, c)
+    a, b = y.float().cpu().numpy(), y2.float().cpu().numpy()
+    assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.nan_to_num(a), np.nan_to_num(b))
+    assert lh.lh_nvfp4_status() == 0
+
+
 def test_linear_of_tokens_that_are_not_finite(cuda_ok):
     rng = np.random.default_rng(2)
     w, wv, wg = bank(rng, 1, 200, 128)
