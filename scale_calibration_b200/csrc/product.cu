@@ -44,6 +44,7 @@ struct ProdArgs {
     int mtiles128;           // rows of scale tiles per matrix
     int stages_k;            // stages along c_in
     int steps;               // 64-column steps along c_in
+    int box;                 // tokens of one TMA copy (single CTAs): a tile brings the rows it has, rounded up to these
     const uint8_t* xs;       // scale tiles of the tokens
     const uint8_t* ws;       // scale tiles of the weights
     const float* xg;         // [n_rows]
@@ -58,7 +59,6 @@ struct ProdArgs {
 };
 
 constexpr int kT = 128;            // tokens of a tile: one scale tile
-constexpr int kBox = 32;           // tokens of one TMA copy: a tile brings the rows it has, rounded up to these
 
 struct Shape {
     static constexpr int kA = kM * kRowBytes, kB = kT * kRowBytes, kSa = 4 * kTileBytes, kSb = 4 * kTileBytes;
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
             const int wsrow = (int)((t.g * p.mtiles + t.mt) * p.steps);
             const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
-            const int boxes = (t.rows + kBox - 1) / kBox;
-            const uint32_t bytes = S::kA + S::kSa + (kFused ? 0 : boxes * kBox * kRowBytes + S::kSb);
+            const int boxes = (t.rows + p.box - 1) / p.box;
+            const uint32_t bytes = S::kA + S::kSa + (kFused ? 0 : boxes * p.box * kRowBytes + S::kSb);
             auto weights = [&](int s, int ks) {
                 const uint32_t bar = smem_u32(&C.full[s]), a = ring + s * S::kStageBytes;
                 mbar_expect_tx(bar, bytes);
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     if (ahead == 0) weights(stage, ks);
                     if constexpr (!kFused) {
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(b + i * kBox * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * kBox, bar);
+                            tma_load_2d(b + i * p.box * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * p.box, bar);
                         tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
                     }
                 }
@@ -791,7 +791,7 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     CUtensorMap wmap, xmap, wsmap, xsmap;
     bool ok = make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) && make_scale_map(encode, &wsmap, p.ws, ws_tiles);
     if constexpr (std::is_void_v<Tin>)
-        ok = ok && make_map(encode, &xmap, X, p.n_rows, c_in / 2, kBox) && make_scale_map(encode, &xsmap, p.xs, xs_tiles);
+        ok = ok && make_map(encode, &xmap, X, p.n_rows, c_in / 2, p.box) && make_scale_map(encode, &xsmap, p.xs, xs_tiles);
     else
         xmap = wmap, xsmap = wsmap;  // not used
     if (!ok) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -915,6 +915,10 @@ ProdArgs product_args(const uint8_t* X_scales, const float* X_gscale, const uint
     p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
     p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
     p.steps = (int)scale_steps(c_in);
+    // the power of 2 that takes a group of average size in one copy (a copy costs its rows,
+    // used or not, about 1.3 ns each)
+    p.box = 16;
+    while (p.box < kT && p.box * n_groups < n_rows) p.box *= 2;
     p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y; p.early = early;
     return p;
 }
