@@ -1,10 +1,15 @@
 """Local-Hessian NVFP4 block-scale calibration for B200 (sm_100a).
 
 The work happens in liblh.so (C ABI in include/lh.h); this package is its
-ctypes binding plus `calibrate`, which chains the four calls of the hot path
-for one layer:
+binding plus `calibrate`, which chains the four calls of the hot path for one
+layer:
 
     lh_absmax -> lh_accumulate_hessian -> lh_sweep_scales_ws -> lh_fake_quant
+
+`calibrate_routed` does so for an expert bank from the router's choices
+(lh_route_tokens -> lh_gather_tokens first), and `QuantizedLayer` runs what was
+calibrated (lh_quantize_nvfp4 and lh_nvfp4_tile_scales once, then
+lh_nvfp4_linear, with lh_combine_tokens for a bank).
 
 Method: "NVIDIA Model Optimizer Local-Hessian: 基于局部 Hessian 的 NVFP4 逐块
 权重缩放算法实战指南" (xxmr.cn/news/266017), sections "算法原理" and
@@ -75,3 +80,149 @@ def calibrate(W, X, offsets=None, out_dtype=None, stream=None):
                      device=W.device)
     codes, amax, Wq = cal.run(W, X, offsets, stream)
     return dict(codes=codes, best_amax=amax, Wq=Wq, H=cal.H, global_amax=cal.amax)
+
+
+def _on_current_device(**tensors):
+    """The library works on the current device; a tensor of another one would be read through the wrong context."""
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, what):
+    """t with 16-byte aligned rows, copied if it has none."""
+    import torch
+    per = 16 // t.element_size()
+    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what} must be a bf16 or f32 matrix")
+    if t.stride(1) == 1 and t.stride(0) % per == 0 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0:
+        return t
+    out = torch.empty(t.shape[0], -(-max(t.shape[1], 1) // per) * per, dtype=t.dtype, device=t.device)[:, :t.shape[1]]
+    return out.copy_(t)
+
+
+class Routing:
+    """Tokens sorted by expert (lh_route_tokens): `offsets` int64 [n_experts + 1], `order` (flat slot t * k + s of each
+    sorted row) and its inverse `pos`, int32 [n_tok * k]. expert_ids: int32 CUDA tensor [n_tok, k]; ids outside
+    [0, n_experts) are slots without an expert. `route` may be called again with other ids of the same shape."""
+
+    def __init__(self, n_tok: int, k: int, n_experts: int, device="cuda"):
+        import torch
+        self.n_tok, self.k, self.n_experts = n_tok, k, n_experts
+        self.offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=device)
+        self.order = torch.empty(n_tok * k, dtype=torch.int32, device=device)
+        self.pos = torch.empty(n_tok * k, dtype=torch.int32, device=device)
+
+    def route(self, expert_ids, stream=None):
+        import torch
+        if expert_ids.dtype != torch.int32 or tuple(expert_ids.shape) != (self.n_tok, self.k):
+            raise ValueError(f"expert_ids must be int32 [{self.n_tok}, {self.k}]")
+        _on_current_device(expert_ids=expert_ids, offsets=self.offsets)
+        lh_route_tokens(expert_ids.contiguous(), self.n_tok, self.k, self.n_experts, self.offsets, self.order, self.pos,
+                        stream)
+        return self
+
+
+def calibrate_routed(W, X, expert_ids, out_dtype=None, stream=None):
+    """Local-Hessian calibration of an expert bank W [n_experts, c_out, c_in] from unsorted tokens X [n_tok, c_in]
+    (bf16) and the experts that each was routed to (int32 [n_tok, k]): calibrate() on the sorted rows. Experts without
+    tokens have H = 0 (every block gets code 1)."""
+    import torch
+    _on_current_device(W=W, X=X, expert_ids=expert_ids)
+    n_tok, k = expert_ids.shape
+    if X.shape[0] != n_tok or X.shape[1] != W.shape[2]:
+        raise ValueError("X must be [n_tok, c_in]")
+    X = _rows(X, "X")
+    r = Routing(n_tok, k, W.shape[0], W.device).route(expert_ids, stream)
+    # rows of slots without an expert lie behind the last group and are never used
+    rows = torch.empty(n_tok * k, W.shape[2], dtype=X.dtype, device=X.device)
+    lh_gather_tokens(X, X, n_tok, X.shape[1], X.stride(0), r.order, k, n_tok * k, rows, rows.stride(0), stream)
+    return calibrate(W, rows, r.offsets, out_dtype, stream)
+
+
+class QuantizedLayer:
+    """A calibrated layer in NVFP4, run with NVFP4 tokens (W4A4): Y = Xq Wq^T.
+
+    W [n_mats, c_out, c_in] (or one matrix [c_out, c_in]), global_amax and codes as `calibrate` returns them;
+    x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None for one scale per token. The packed
+    weights and their scale tiles are made once. Workspaces are kept per number of rows and belong to the layer: run it
+    on one stream at a time, and give graphs that may run at the same time layers of their own
+    (`shared_copy`)."""
+
+    def __init__(self, W, global_amax, codes, x_amax=None, stream=None):
+        import torch
+        if W.dim() == 2:
+            W = W.unsqueeze(0)
+        _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
+        self.n_mats, self.c_out, self.c_in = W.shape
+        if self.c_in % 32:
+            raise ValueError(f"c_in={self.c_in} is not a multiple of 32")
+        J = self.c_in // 16
+        codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
+        W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
+        dev = W.device
+        self.packed = torch.empty(self.n_mats, self.c_out, self.c_in // 2, dtype=torch.uint8, device=dev)
+        self.block_scales = torch.empty_like(codes)
+        self.global_scale = torch.empty(self.n_mats, dtype=torch.float32, device=dev)
+        self.scale_tiles = torch.empty(lh_nvfp4_weight_scale_bytes(self.n_mats, self.c_out, self.c_in),
+                                       dtype=torch.uint8, device=dev)
+        lh_quantize_nvfp4(W, W, self.n_mats, self.c_out, self.c_in, W.stride(1), global_amax, codes, self.packed,
+                          self.block_scales, self.global_scale, stream=stream)
+        lh_nvfp4_tile_scales(self.block_scales, self.n_mats, self.c_out, self.c_in, self.scale_tiles, stream)
+        self.x_amax = x_amax
+        self._ws = {}
+
+    def shared_copy(self):
+        """A layer of the same weights with workspaces of its own."""
+        import copy
+        other = copy.copy(self)
+        other._ws = {}
+        return other
+
+    def _linear(self, X, rows, row_div, n_rows, offsets, out_dtype, stream):
+        import torch
+        X = _rows(X, "X")
+        if X.shape[1] != self.c_in:
+            raise ValueError(f"X has {X.shape[1]} columns, the layer takes {self.c_in}")
+        _on_current_device(X=X, packed=self.packed, rows=rows, offsets=offsets)
+        out_dtype = out_dtype or X.dtype
+        per = 8 if out_dtype == torch.bfloat16 else 4
+        Y = torch.empty(n_rows, -(-self.c_out // per) * per, dtype=out_dtype, device=X.device)[:, :self.c_out]
+        if n_rows == 0:
+            return Y
+        need = lh_nvfp4_linear_workspace_bytes(n_rows, self.c_in, self.n_mats)
+        ws = self._ws.get(n_rows)
+        if ws is None:
+            ws = self._ws[n_rows] = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+        lh_nvfp4_linear(X, X, X.shape[0], self.c_in, X.stride(0), rows, row_div, n_rows, offsets, self.n_mats,
+                        self.x_amax, self.packed, self.scale_tiles, self.global_scale, self.c_out, Y, Y, Y.stride(0), ws,
+                        need, stream)
+        return Y
+
+    def forward(self, X, offsets=None, out_dtype=None, stream=None):
+        """Y [n_tok, c_out] of X [n_tok, c_in]; with several matrices the tokens of each are those of its group
+        (offsets int64 [n_mats + 1] on the device); rows of tokens in no group are left unset."""
+        if (offsets is None) != (self.n_mats == 1):
+            raise ValueError("several matrices need offsets, and one takes none")
+        return self._linear(X, None, 1, X.shape[0], offsets, out_dtype, stream)
+
+    __call__ = forward
+
+    def forward_routed(self, X, routing: Routing, weights=None, out_dtype=None, stream=None):
+        """The bank's output for tokens X [n_tok, c_in]: sum over a token's experts of weights[t, s] (f32 [n_tok, k], or
+        None for ones) times the expert's product. A token without any expert gets zeros."""
+        import torch
+        n_tok, k = routing.n_tok, routing.k
+        if X.shape[0] != n_tok or routing.n_experts != self.n_mats:
+            raise ValueError("the routing is for another number of tokens or experts")
+        if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (n_tok, k)):
+            raise ValueError(f"weights must be f32 [{n_tok}, {k}]")
+        rows = self._linear(X, routing.order, k, n_tok * k, routing.offsets, out_dtype, stream)
+        Y = torch.empty(n_tok, rows.stride(0), dtype=rows.dtype, device=X.device)[:, :self.c_out]
+        if n_tok == 0:
+            return Y
+        weights = weights.contiguous() if weights is not None else None
+        lh_combine_tokens(rows, rows, n_tok * k, self.c_out, rows.stride(0), routing.pos, weights, n_tok, k, Y,
+                          Y.stride(0), stream)
+        return Y
