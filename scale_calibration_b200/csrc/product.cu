@@ -91,7 +91,7 @@ struct Tile {
 template <int T>
 struct Walk {
     int64_t g = 0;
-    int base = 0;  // tiles before group g
+    int64_t base = 0;  // tiles before group g
     __device__ void range(const ProdArgs& p, int64_t i, int64_t& lo, int64_t& hi) const {
         if (!p.offsets) {
             lo = 0;
@@ -103,26 +103,27 @@ struct Walk {
         lo = lo < 0 ? 0 : (lo > p.n_rows ? p.n_rows : lo);
         hi = hi < 0 ? 0 : (hi > p.n_rows ? p.n_rows : hi);
     }
-    __device__ bool find(const ProdArgs& p, int u, Tile& t) {
+    __device__ bool find(const ProdArgs& p, int64_t u, Tile& t) {
         const int lane = threadIdx.x & 31;
         while (g < p.G) {
             int64_t lo = 0, hi = 0;
             if (g + lane < p.G) range(p, g + lane, lo, hi);
-            const int nt = hi > lo ? (int)((hi - lo + T - 1) / T) * p.mtiles : 0;
-            int inc = nt;
+            // sums stop at 2^32 - 1: groups that overlap (decreasing offsets) can have more tiles
+            uint32_t inc = hi > lo ? (uint32_t)((hi - lo + T - 1) / T) * p.mtiles : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if (lane >= o) inc += v;
+                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc = inc + v < v ? 0xFFFFFFFFu : inc + v;
             }
             const uint32_t hit = __ballot_sync(0xFFFFFFFFu, base + inc > u);
             if (hit) {
                 const int l = __ffs(hit) - 1;
-                base += __shfl_sync(0xFFFFFFFFu, inc - nt, l);
+                const uint32_t before = __shfl_sync(0xFFFFFFFFu, inc, l ? l - 1 : 0);
+                base += l ? before : 0;
                 g += l;
                 lo = __shfl_sync(0xFFFFFFFFu, lo, l);
                 hi = __shfl_sync(0xFFFFFFFFu, hi, l);
-                const int i = u - base;
+                const int i = (int)(u - base);
                 const int tt = i / p.mtiles;
                 t.g = g;
                 t.lo = lo;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int u = first; ok && walk.find(p, u, t); u += step) {
+        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
             const int wsrow = (int)((t.g * p.mtiles + t.mt) * p.steps);
             const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int stage = 0, acc = 0;
         uint32_t phase = 0, aphase = 0, set = 0;
         bool ok = true;
-        for (int u = first; ok && walk.find(p, u, t); u += step) {
+        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
             if (!ok) break;
             fence_after();
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
-        for (int u = first; ok && walk.find(p, u, t); u += step) {
+        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const float gw = __ldg(p.wg + t.g);
             float gx[4];
 #pragma unroll
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int u = first; ok && walk.find(p, u, t); u += step) {
+        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int half = ((t.rows + 15) & ~15) / 2;  // tokens that each CTA brings
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * 2 * kM + rank * kM);
             const int xrow = (int)t.row0 + (int)rank * half;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int stage = 0;
             uint32_t phase = 0, aphase = 0, set = 0;
             bool ok = true;
-            for (int u = first; ok && walk.find(p, u, t); u += step) {
+            for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
                 ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
                 if (!ok) break;
                 fence_after();
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
         uint32_t aphase = 0;
         bool ok = true;
-        for (int u = first; ok && walk.find(p, u, t); u += step) {
+        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int64_t ch0 = (int64_t)t.mt * 2 * kM + rank * kM + q * 32;
             const float gw = __ldg(p.wg + t.g);
             const int c0 = h * (kPairT / 2);

@@ -448,6 +448,54 @@ def test_product_of_quantised_tokens(cuda_ok, n, m, c, t):
     assert (err <= ref.product_tolerance(want, s, c, t == "bf16")).all()
 
 
+def test_decreasing_offsets_stay_in_bounds(cuda_ok):
+    # results are unspecified, but nothing outside the rows that some group names is touched
+    lh = _lh()
+    rng = np.random.default_rng(0)
+    n, m, c = 500, 130, 96
+    w, _, _ = bank(rng, 4, m, c)
+    x = torch.from_numpy(rng.standard_normal((n, c)).astype(np.float32)).cuda()
+    for off in ([10, 300, 20, 260, 100], [-50, 40, 10 ** 12, 3, 200], [400, 300, 200, 100, 50]):
+        y = torch.full((n + 8, pitch(m, "f32")), 6.0, device="cuda")
+        linear(x, n, c, w, m, y[:n], off=torch.tensor(off, dtype=torch.int64, device="cuda"))
+        assert lh.lh_nvfp4_status() == 0
+        named = np.zeros(n + 8, bool)
+        for a, b in zip(off, off[1:]):
+            named[max(min(a, n), 0):max(min(b, n), 0)] = True
+        assert (y[torch.from_numpy(~named).cuda()] == 6.0).all() and (y[:, m:] == 6.0).all()
+
+
+def test_outputs_beyond_32_bits(cuda_ok):
+    # offsets in Y, in the quantised values and in gathered rows past 2^32 bytes: the far rows equal the near ones
+    lh = _lh()
+    rng = np.random.default_rng(5)
+    w, _, _ = bank(rng, 1, 66000, 32)
+    n = 34000
+    near = torch.from_numpy(rng.standard_normal((200, 32)).astype(np.float32)).cuda()
+    x = near.repeat(n // 200, 1).contiguous()
+    y = torch.zeros(n, 66000, dtype=torch.bfloat16, device="cuda")
+    linear(x, n, 32, w, 66000, y)
+    assert torch.equal(y[-200:], y[:200]) and torch.equal(y[n // 2 // 200 * 200:][:200], y[:200])
+    assert float(y[:200].float().abs().sum()) > 0
+    del y, w
+    n, c = 40000, 32768
+    x = torch.from_numpy(rng.standard_normal((8, c)).astype(np.float32)).cuda()
+    src = (torch.arange(n, device="cuda") % 8).to(torch.int32)
+    packed, _, g, values = quantize(x, 8, c, src, 1, n, out=torch.float32)
+    assert torch.equal(values[-8:], values[:8]) and torch.equal(packed[-8:], packed[:8]) and torch.equal(g[-8:], g[:8])
+    rows = torch.zeros_like(values)
+    lh.lh_gather_tokens(x, x, 8, c, c, src, 1, n, rows, c)
+    assert torch.equal(rows[-8:], x) and torch.equal(rows[:8], x)
+    back = torch.zeros(2, c, device="cuda")
+    pos = torch.tensor([n - 8, n - 7, n - 6, -1], dtype=torch.int32, device="cuda")
+    lh.lh_combine_tokens(rows, rows, n, c, c, pos, None, 2, 2, back, c)
+    assert torch.equal(back[1], x[2]) and torch.equal(back[0], x[0] + x[1])
+    dw = torch.zeros(2, 2, device="cuda")
+    lh.lh_combine_tokens_grad(back, back, 2, 2, c, c, rows, c, n, pos, None, None, 0, dw)
+    want = (back[1].double() * x[2].double()).sum()
+    assert abs(float(dw[1, 0]) - float(want)) <= (c + 5) * 2.0 ** -24 * float((back[1].double() * x[2].double()).abs().sum())
+
+
 def test_every_scale_code_multiplies_by_its_value(cuda_ok):
     # token r has block scale code r + 1 and values 1; the weights are 1 with scale 1: each output is 32 v(r + 1), exact
     c, m = 32, 8
