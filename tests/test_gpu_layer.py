@@ -408,7 +408,8 @@ def test_product_of_whole_numbers_is_exact(cuda_ok, n, m, c, t):
     ([1], 0, 0, 128, 256), ([0, 1, 0, 0, 3], 0, 0, 96, 64), ([5, 17, 130, 0, 1, 300], 0, 0, 200, 544),
     ([128, 256, 129], 2, 7, 257, 96), ([0] * 70 + [2, 1] + [0] * 30 + [33], 0, 5, 64, 128), ([0, 0], 4, 0, 32, 32),
     ([1] * 100, 0, 0, 130, 1024), ([300, 700, 0, 513, 16], 5, 3, 300, 352), ([1024, 1], 0, 0, 520, 128),
-    ([40, 0, 33, 2, 65], 0, 0, 70, 4352), ([64, 31, 97, 255, 2], 1, 1, 384, 2048),
+    ([40, 0, 33, 2, 65], 0, 0, 70, 4352),
+    ([257, 20, 300, 500, 33, 1, 2000, 129, 160], 1, 4, 400, 288), ([3000, 32, 31, 33, 97], 0, 0, 1152, 64), ([64, 31, 97, 255, 2], 1, 1, 384, 2048),
 ])
 def test_grouped_product_of_whole_numbers_is_exact(cuda_ok, counts, before, after, m, c, t):
     rng = np.random.default_rng(len(counts) + m)
