@@ -246,14 +246,19 @@ struct Vec {
     }
 };
 
-// This thread's (row, vector) with `per` vectors a row: a 64-bit division for the CTA's
-// first vector, the same in all its threads, and a 32-bit one for each thread.
+// This thread's (row, vector) with `per` vectors a row, of the CTA's vectors from `first`
+// on: a division for each thread, of 32 bits where it can be (one of 64 bits takes as long
+// as all the rest).
 __device__ __forceinline__ void split(int64_t first, uint32_t per, int64_t& row, uint32_t& v) {
-    const int64_t row0 = first / per;
-    const uint32_t i = (uint32_t)(first - row0 * per) + threadIdx.x;
-    const uint32_t r = i / per;
-    row = row0 + r;
-    v = i - r * per;
+    if (first <= 0xFFFFFFFFll - kRowThreads) {
+        const uint32_t i = (uint32_t)first + threadIdx.x, r = i / per;
+        row = r;
+        v = i - r * per;
+    } else {
+        const int64_t i = first + threadIdx.x;
+        row = i / per;
+        v = (uint32_t)(i - row * per);
+    }
 }
 
 template <typename T, int kBytes>
