@@ -417,6 +417,7 @@ LH_API lh_status lh_nvfp4_tile_scales(const uint8_t* block_scales, int64_t n_mat
  *   [0, n_rows]. Decreasing offsets are not detected: accesses stay in bounds, results
  *   are unspecified. Outputs of rows that lie in no group, and of rows whose source is
  *   negative or past n_src, are left as they were.
+ * c_in: a multiple of 16, at most 2^28. n_rows and n_groups below 2^31 - 512.
  * X: device bf16 or f32 [n_src][ld_x]. rows: device int32 [n_rows] or NULL.
  * global_amax: device f32 [1] or NULL. packed: device u8 [n_rows][c_in/2], 16-byte
  *   aligned. scale_tiles: device, 16-byte aligned, lh_nvfp4_token_scale_bytes(n_rows,

@@ -90,6 +90,16 @@ def _on_current_device(**tensors):
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _on(stream):
+    """Makes `stream` (a torch stream, its handle, or None for the current one) current, so that what is allocated for
+    its kernels is not handed out again before they are done."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _rows(t, what):
     """t with 16-byte aligned rows, copied if it has none."""
     import torch
@@ -119,8 +129,8 @@ class Routing:
         if expert_ids.dtype != torch.int32 or tuple(expert_ids.shape) != (self.n_tok, self.k):
             raise ValueError(f"expert_ids must be int32 [{self.n_tok}, {self.k}]")
         _on_current_device(expert_ids=expert_ids, offsets=self.offsets)
-        lh_route_tokens(expert_ids.contiguous(), self.n_tok, self.k, self.n_experts, self.offsets, self.order, self.pos,
-                        stream)
+        with _on(stream):
+            lh_route_tokens(expert_ids.contiguous(), self.n_tok, self.k, self.n_experts, self.offsets, self.order, self.pos)
         return self
 
 
@@ -133,12 +143,13 @@ def calibrate_routed(W, X, expert_ids, out_dtype=None, stream=None):
     n_tok, k = expert_ids.shape
     if X.shape[0] != n_tok or X.shape[1] != W.shape[2]:
         raise ValueError("X must be [n_tok, c_in]")
-    X = _rows(X, "X")
-    r = Routing(n_tok, k, W.shape[0], W.device).route(expert_ids, stream)
-    # rows of slots without an expert lie behind the last group and are never used
-    rows = torch.empty(n_tok * k, W.shape[2], dtype=X.dtype, device=X.device)
-    lh_gather_tokens(X, X, n_tok, X.shape[1], X.stride(0), r.order, k, n_tok * k, rows, rows.stride(0), stream)
-    return calibrate(W, rows, r.offsets, out_dtype, stream)
+    with _on(stream):
+        X = _rows(X, "X")
+        r = Routing(n_tok, k, W.shape[0], W.device).route(expert_ids)
+        # rows of slots without an expert lie behind the last group and are never used
+        rows = torch.empty(n_tok * k, W.shape[2], dtype=X.dtype, device=X.device)
+        lh_gather_tokens(X, X, n_tok, X.shape[1], X.stride(0), r.order, k, n_tok * k, rows, rows.stride(0))
+        return calibrate(W, rows, r.offsets, out_dtype)
 
 
 class QuantizedLayer:
@@ -146,9 +157,8 @@ class QuantizedLayer:
 
     W [n_mats, c_out, c_in] (or one matrix [c_out, c_in]), global_amax and codes as `calibrate` returns them;
     x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None for one scale per token. The packed
-    weights and their scale tiles are made once. Workspaces are kept per number of rows and belong to the layer: run it
-    on one stream at a time, and give graphs that may run at the same time layers of their own
-    (`shared_copy`)."""
+    weights and their scale tiles are made once; every call has a workspace of its own from torch's allocator, so calls
+    on several streams and captured graphs do not share one."""
 
     def __init__(self, W, global_amax, codes, x_amax=None, stream=None):
         import torch
@@ -159,28 +169,21 @@ class QuantizedLayer:
         if self.c_in % 32:
             raise ValueError(f"c_in={self.c_in} is not a multiple of 32")
         J = self.c_in // 16
-        codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
-        W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
-        dev = W.device
-        self.packed = torch.empty(self.n_mats, self.c_out, self.c_in // 2, dtype=torch.uint8, device=dev)
-        self.block_scales = torch.empty_like(codes)
-        self.global_scale = torch.empty(self.n_mats, dtype=torch.float32, device=dev)
-        self.scale_tiles = torch.empty(lh_nvfp4_weight_scale_bytes(self.n_mats, self.c_out, self.c_in),
-                                       dtype=torch.uint8, device=dev)
-        lh_quantize_nvfp4(W, W, self.n_mats, self.c_out, self.c_in, W.stride(1), global_amax, codes, self.packed,
-                          self.block_scales, self.global_scale, stream=stream)
-        lh_nvfp4_tile_scales(self.block_scales, self.n_mats, self.c_out, self.c_in, self.scale_tiles, stream)
+        with _on(stream):
+            codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
+            W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
+            dev = W.device
+            self.packed = torch.empty(self.n_mats, self.c_out, self.c_in // 2, dtype=torch.uint8, device=dev)
+            self.block_scales = torch.empty_like(codes)
+            self.global_scale = torch.empty(self.n_mats, dtype=torch.float32, device=dev)
+            self.scale_tiles = torch.empty(lh_nvfp4_weight_scale_bytes(self.n_mats, self.c_out, self.c_in),
+                                           dtype=torch.uint8, device=dev)
+            lh_quantize_nvfp4(W, W, self.n_mats, self.c_out, self.c_in, W.stride(1), global_amax, codes, self.packed,
+                              self.block_scales, self.global_scale)
+            lh_nvfp4_tile_scales(self.block_scales, self.n_mats, self.c_out, self.c_in, self.scale_tiles)
         self.x_amax = x_amax
-        self._ws = {}
 
-    def shared_copy(self):
-        """A layer of the same weights with workspaces of its own."""
-        import copy
-        other = copy.copy(self)
-        other._ws = {}
-        return other
-
-    def _linear(self, X, rows, row_div, n_rows, offsets, out_dtype, stream):
+    def _linear(self, X, rows, row_div, n_rows, offsets, out_dtype):
         import torch
         X = _rows(X, "X")
         if X.shape[1] != self.c_in:
@@ -192,12 +195,10 @@ class QuantizedLayer:
         if n_rows == 0:
             return Y
         need = lh_nvfp4_linear_workspace_bytes(n_rows, self.c_in, self.n_mats)
-        ws = self._ws.get(n_rows)
-        if ws is None:
-            ws = self._ws[n_rows] = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=X.device)
         lh_nvfp4_linear(X, X, X.shape[0], self.c_in, X.stride(0), rows, row_div, n_rows, offsets, self.n_mats,
                         self.x_amax, self.packed, self.scale_tiles, self.global_scale, self.c_out, Y, Y, Y.stride(0), ws,
-                        need, stream)
+                        need)
         return Y
 
     def forward(self, X, offsets=None, out_dtype=None, stream=None):
@@ -205,7 +206,8 @@ class QuantizedLayer:
         (offsets int64 [n_mats + 1] on the device); rows of tokens in no group are left unset."""
         if (offsets is None) != (self.n_mats == 1):
             raise ValueError("several matrices need offsets, and one takes none")
-        return self._linear(X, None, 1, X.shape[0], offsets, out_dtype, stream)
+        with _on(stream):
+            return self._linear(X, None, 1, X.shape[0], offsets, out_dtype)
 
     __call__ = forward
 
@@ -218,11 +220,13 @@ class QuantizedLayer:
             raise ValueError("the routing is for another number of tokens or experts")
         if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (n_tok, k)):
             raise ValueError(f"weights must be f32 [{n_tok}, {k}]")
-        rows = self._linear(X, routing.order, k, n_tok * k, routing.offsets, out_dtype, stream)
-        Y = torch.empty(n_tok, rows.stride(0), dtype=rows.dtype, device=X.device)[:, :self.c_out]
-        if n_tok == 0:
+        _on_current_device(weights=weights)
+        with _on(stream):
+            rows = self._linear(X, routing.order, k, n_tok * k, routing.offsets, out_dtype)
+            Y = torch.empty(n_tok, rows.stride(0), dtype=rows.dtype, device=X.device)[:, :self.c_out]
+            if n_tok == 0:
+                return Y
+            weights = weights.contiguous() if weights is not None else None
+            lh_combine_tokens(rows, rows, n_tok * k, self.c_out, rows.stride(0), routing.pos, weights, n_tok, k, Y,
+                              Y.stride(0))
             return Y
-        weights = weights.contiguous() if weights is not None else None
-        lh_combine_tokens(rows, rows, n_tok * k, self.c_out, rows.stride(0), routing.pos, weights, n_tok, k, Y,
-                          Y.stride(0), stream)
-        return Y

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
         const bool bad_token = mb >= 0x7F800000u;
         const RowScale rs(kGiven ? __ldg(p.gamax) : __uint_as_float(mb));
         const uint32_t r = row - lo, rt = r % kTileRows;
-        uint8_t* tiles = p.tiles + (uint64_t)((uint32_t)lo / kTileRows + g + r / kTileRows) * (uint32_t)(p.steps * kTileBytes) +
+        uint8_t* tiles = p.tiles + (uint64_t)((uint32_t)lo / kTileRows + g + r / kTileRows) * ((uint32_t)p.steps * kTileBytes) +
                          (rt % 32) * 16 + rt / 32 * 4;
         const int64_t out0 = (int64_t)row * J;
         for (int j0 = tid; j0 - tid < 4 * p.steps; j0 += kSpan * kN) {
@@ -266,7 +266,7 @@ lh_status check_tokens(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c
         return fail(LH_ERR_ALIGNMENT, "X must be 16-byte aligned with 16-byte aligned rows");
     if (!aligned16(packed) || !aligned16(scale_tiles) || !aligned16(X_out))
         return fail(LH_ERR_ALIGNMENT, "packed, scale_tiles and X_out must be 16-byte aligned");
-    if (c_in > INT_MAX - 64) return fail(LH_ERR_UNSUPPORTED, "c_in must be below 2^31 - 64");
+    if (c_in > (1 << 28)) return fail(LH_ERR_UNSUPPORTED, "c_in must be at most 2^28");  // a row of scale tiles: 2^31 bytes
     if (X == X_out || X == (const void*)packed || X == (const void*)scale_tiles || packed == scale_tiles)
         return fail(LH_ERR_INVALID_ARG, "outputs must not alias X or one another");
     return LH_OK;

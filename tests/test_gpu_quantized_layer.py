@@ -49,8 +49,9 @@ def test_a_calibrated_layer_runs(cuda_ok, dtype, given):
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         y2 = q(x)
+    y3, y4 = q(x, stream=s), q(x, stream=s.cuda_stream)
     s.synchronize()
-    assert torch.equal(y2, y)
+    assert torch.equal(y2, y) and torch.equal(y3, y) and torch.equal(y4, y)
 
 
 def test_a_routed_bank_is_calibrated_and_runs(cuda_ok):
@@ -82,16 +83,15 @@ def test_a_routed_bank_is_calibrated_and_runs(cuda_ok):
     tol += (np.abs(want) + tol) * (2.0 ** -8 + k * 2.0 ** -24) + 1e-30
     assert (np.abs(y - want) <= tol).all()
     assert (y[7] == 0).all()
-    # two copies of the layer in two graphs that run at the same time, against the layer alone
-    other = q.shared_copy()
+    # the layer in two graphs that run at the same time, against the layer alone
     x2 = (X * 2).contiguous()
-    q.forward_routed(X, r, w), other.forward_routed(x2, r, w)
+    q.forward_routed(X, r, w), q.forward_routed(x2, r, w)
     torch.cuda.synchronize()
     ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
     with torch.cuda.graph(ga):
         ya = q.forward_routed(X, r, w)
     with torch.cuda.graph(gb):
-        yb = other.forward_routed(x2, r, w)
+        yb = q.forward_routed(x2, r, w)
     sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
     for _ in range(20):
         with torch.cuda.stream(sa):

@@ -131,7 +131,8 @@ def test_quantize_tokens_refusals():
         (dict(n_rows=11), 1), (dict(c_in=40, ld_x=40), 2), (dict(ld_x=48), 1), (dict(ld_x=68), 3), (dict(X=FAKE + 8), 3),
         (dict(packed=FAKE + 65544), 3), (dict(scale_tiles=FAKE + 131080), 3), (dict(X_out=FAKE + 8), 3),
         (dict(X_out=FAKE), 1), (dict(packed=FAKE), 1), (dict(scale_tiles=FAKE + 65536), 1), (dict(x_dtype=3), 2),
-        (dict(X_out=FAKE + 524288, out_dtype=3), 2),
+        (dict(X_out=FAKE + 524288, out_dtype=3), 2), (dict(c_in=(1 << 28) + 16, ld_x=(1 << 28) + 16), 2),
+        (dict(n_src=1 << 31, n_rows=1 << 31), 2), (dict(row_div=1 << 31, rows=FAKE), 2),
     ])
     for over in (dict(n_rows=0), dict(c_in=0)):
         assert lh.lh_quantize_tokens(**dict(ok, **over)) == 0
