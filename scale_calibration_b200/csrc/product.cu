@@ -93,17 +93,21 @@ struct Walk {
     int64_t g = 0;
     int64_t base = 0;  // tiles before group g
     __device__ void range(const ProdArgs& p, int64_t i, int64_t& lo, int64_t& hi) const {
-        if (!p.offsets) {
-            lo = 0;
-            hi = p.n_rows;
-            return;
-        }
         lo = __ldg(p.offsets + i);
         hi = __ldg(p.offsets + i + 1);
         lo = lo < 0 ? 0 : (lo > p.n_rows ? p.n_rows : lo);
         hi = hi < 0 ? 0 : (hi > p.n_rows ? p.n_rows : hi);
     }
     __device__ bool find(const ProdArgs& p, int64_t u, Tile& t) {
+        if (!p.offsets) {
+            const uint32_t tt = (uint32_t)u / (uint32_t)p.mtiles;
+            t.g = t.lo = 0;
+            t.mt = (int)((uint32_t)u - tt * p.mtiles);
+            t.row0 = (int64_t)tt * T;
+            t.sub = (int)t.row0;
+            t.rows = p.n_rows - t.row0 < T ? (int)(p.n_rows - t.row0) : T;
+            return t.row0 < p.n_rows;
+        }
         const int lane = threadIdx.x & 31;
         while (g < p.G) {
             int64_t lo = 0, hi = 0;
@@ -670,6 +674,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int stage = 0;
             uint32_t phase = 0, aphase = 0, set = 0;
             bool ok = true;
+            const uint64_t desc_a = desc_k_sw128(ring), desc_b = desc_k_sw128(ring + S::kA);
+            const uint64_t desc_sa = desc_scales(ring + S::kA + S::kB), desc_sb = desc_scales(ring + S::kA + S::kB + S::kSa);
             for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
                 ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
                 if (!ok) break;
@@ -682,18 +688,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     fence_after();
                     if (elect_one()) {
                         const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                        const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB,
-                                       sb = sa + S::kSa;
-                        const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                        const uint32_t at = stage * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
+                        const uint32_t ca = S::kScaleCol + set * S::kSetCols, cb = ca + 16;
                         // step by step: the copies of a step run beside the products of the one before
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if (k >= nk) break;
-                            tmem_cp_scales_pair(cb + 8 * k, desc_scales(sb + k * kTileBytes));
-                            tmem_cp_scales_pair(cb + 8 * k + 4, desc_scales(sb + (4 + k) * kTileBytes));
-                            tmem_cp_scales_pair(ca + 4 * k, desc_scales(sa + k * kTileBytes));
-                            mma_nvfp4_pair(tmem, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
-                                           cb + 8 * k, (ks | k) ? 1u : 0u);
+                            tmem_cp_scales_pair(cb + 8 * k, desc_sb + (at + k * (kTileBytes >> 4)));
+                            tmem_cp_scales_pair(cb + 8 * k + 4, desc_sb + (at + (4 + k) * (kTileBytes >> 4)));
+                            tmem_cp_scales_pair(ca + 4 * k, desc_sa + (at + k * (kTileBytes >> 4)));
+                            mma_nvfp4_pair(0, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 8 * k,
+                                           (ks | k) ? 1u : 0u);
                         }
                         mma_commit_pair(smem_u32(&C.empty[stage]));
                         if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
