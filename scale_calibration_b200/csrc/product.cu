@@ -421,6 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int stage = 0, acc = 0;
         uint32_t phase = 0, aphase = 0, set = 0;
         bool ok = true;
+        const uint64_t desc_a = desc_k_sw128(ring), desc_b = desc_k_sw128(ring + S::kA);
+        const uint64_t desc_sa = desc_scales(ring + S::kA + S::kB), desc_sb = desc_scales(ring + S::kA + S::kB + S::kSa);
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
             if (!ok) break;
@@ -428,27 +430,31 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t n16 = (t.rows + 15) & ~15;
             // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
             const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
-            const uint32_t d = tmem + acc * kT;
+            const uint32_t d = acc * kT;
+            bool ready = false;
             for (int ks = ks0; ks < ks1; ++ks) {
-                ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
+                ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
                 if (!ok) break;
                 fence_after();
+                // a first look at the next stage, answered while this one's products are issued
+                const bool last = stage + 1 == S::kStages;
+                const bool seen = mbar_test(smem_u32(&C.full[last ? 0 : stage + 1]), last ? phase ^ 1 : phase);
                 if (elect_one()) {
                     const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
-                    const uint32_t ca = tmem + S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                    const uint32_t at = stage * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
+                    const uint32_t ca = S::kScaleCol + set * S::kSetCols, cb = ca + 16;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k >= nk) break;
-                        tmem_cp_scales(cb + 4 * k, desc_scales(sb + k * kTileBytes));
-                        tmem_cp_scales(ca + 4 * k, desc_scales(sa + k * kTileBytes));
-                        mma_nvfp4(d, desc_k_sw128(a + 32 * k), desc_k_sw128(b + 32 * k), idesc, ca + 4 * k,
-                                  cb + 4 * k, (ks > ks0 || k > 0) ? 1u : 0u);
+                        tmem_cp_scales(cb + 4 * k, desc_sb + (at + k * (kTileBytes >> 4)));
+                        tmem_cp_scales(ca + 4 * k, desc_sa + (at + k * (kTileBytes >> 4)));
+                        mma_nvfp4(d, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 4 * k,
+                                  (ks > ks0 || k > 0) ? 1u : 0u);
                     }
                     mma_commit(smem_u32(&C.empty[stage]));
                     if (ks == ks1 - 1) mma_commit(smem_u32(&C.tfull[acc]));
                 }
-                __syncwarp();
+                ready = __all_sync(0xFFFFFFFFu, seen);
                 set ^= 1;
                 if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
@@ -682,10 +688,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 fence_after();
                 const uint32_t n16 = (t.rows + 15) & ~15;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
+                bool ready = false;
                 for (int ks = 0; ks < p.stages_k; ++ks) {
-                    ok = warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
+                    ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
                     if (!ok) break;
                     fence_after();
+                    // a first look at the next stage, answered while this one's products are issued
+                    const bool last = stage + 1 == S::kStages;
+                    const bool seen = mbar_test(smem_u32(&C.full[last ? 0 : stage + 1]), last ? phase ^ 1 : phase);
                     if (elect_one()) {
                         const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
                         const uint32_t at = stage * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         mma_commit_pair(smem_u32(&C.empty[stage]));
                         if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
                     }
-                    __syncwarp();
+                    ready = __all_sync(0xFFFFFFFFu, seen);
                     set ^= 1;
                     if (++stage == S::kStages) { stage = 0; phase ^= 1; }
                 }
