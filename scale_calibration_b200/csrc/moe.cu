@@ -28,7 +28,9 @@ constexpr int kRouteCluster = 8;
 
 using tc::cluster_rank;
 using tc::cluster_size;
+using tc::cluster_arrive;
 using tc::cluster_sync;
+using tc::cluster_wait;
 
 __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
     uint32_t v;
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __re
         wsum[lane] = s;
     }
     __syncthreads();
+    if (ranks > 1) cluster_arrive();  // this CTA has read the others' counts
     inc += warp ? wsum[warp - 1] : 0u;
     if (tid < E) {
         base[tid] = inc - all + before;
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_kernel(const int* __re
     for (int i = 0; i < kHeldIds; ++i) place(f0 + 32 * i + lane, e_held[i], r_held[i]);
     for (int f = f0 + 32 * kHeldIds + lane; f - lane < f1; f += 32) place(f, expert_of(f), f < f1 ? pos[f] : 0);
     for (int64_t p = (int64_t)n_valid + rank * kRouteThreads + tid; p < n; p += ranks * kRouteThreads) order[p] = -1;
-    if (ranks > 1) cluster_sync();  // a CTA's counts stay readable until every CTA has read them
+    if (ranks > 1) cluster_wait();  // a CTA's counts stay readable until every CTA has read them
 }
 
 // ---------------------------------------------------------------- rows

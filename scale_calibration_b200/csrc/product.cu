@@ -66,7 +66,7 @@ struct Shape {
     static constexpr int kStages = 6;
     // TMEM: two accumulators, then the scales of two stages (addresses of scales are
     // multiples of 4 columns, so a tile starts with a scale tile)
-    static constexpr int kScaleCol = 2 * kT, kSetCols = 32, kTmemCols = 512;
+    static constexpr int kScaleCol = 2 * kT, kSetCols = 32, kTmemCols = 512;  // all
     static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "TMEM columns");
     static_assert(kStages * kStageBytes >= 2 * kT * kM * 4, "split: the partial sums reuse the ring");
 };
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         C.abort_flag = 0;
         mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&C.tmem), S::kTmemCols);
+    if (warp == 1) tmem_alloc(smem_u32(&C.tmem), S::kTmemCols);  // all columns: they begin at 0
     fence_before();
     __syncthreads();
     fence_after();
@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
             fence_proxy_async();
         }
-        __syncwarp();
-        cluster_sync();
+        __syncthreads();
+        cluster_meet();  // the rings of all parts are idle
         if (warp >= 2) {
             const uint32_t bar = smem_u32(&C.sums), got = (parts - 1) * tokens_of(rank) * kM * 4;
             if (warp == 2 && elect_one()) {
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
         __syncwarp();
-        cluster_sync();  // nothing is in flight from or to a CTA that ends
+        cluster_meet();  // nothing is in flight from or to a CTA that ends
     }
     fence_before();
     __syncthreads();
@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         C.abort_flag = 0;
         mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc_pair(smem_u32(&C.tmem), 512);
+    if (warp == 1) tmem_alloc_pair(smem_u32(&C.tmem), 512);  // all columns: they begin at 0
     fence_before();
     __syncthreads();
-    cluster_sync();  // the barriers of both CTAs are ready
+    cluster_meet();  // the barriers of both CTAs are ready
     fence_after();
     const uint32_t tmem = C.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -749,6 +749,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             part.take(tmem + ((uint32_t)(q * 32) << 16) + c0, n);
             fence_before();
             __syncwarp();
+            // the values are in registers: no memory is handed over
             if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty), 0));
             aphase ^= 1;
             part.put(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn);
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     fence_before();
     __syncthreads();
-    cluster_sync();  // nothing of the pair is in flight to either CTA
+    cluster_meet();  // nothing of the pair is in flight to either CTA
     fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
