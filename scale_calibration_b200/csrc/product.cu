@@ -172,10 +172,14 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __fl
 // A warp's part of a finished tile: 32 channels (its TMEM lanes) x up to 128 tokens, into
 // registers and from there to Y. Row-major Y wants a token's channels side by side. In f32
 // a lane per channel does that (128 bytes a store). In bf16 the values are taken in the
-// layout of mma fragments and turned by stmatrix through 32 rows of 64 bytes of shared
-// memory (their 16-byte pieces swapped by the row's number, which keeps both ways free of
-// bank conflicts), so that a lane stores 8 channels at once.
-constexpr int kTurnRow = 64, kTurnBytes = 32 * kTurnRow;
+// layout of mma fragments and turned by stmatrix through shared memory, 32 tokens at a time,
+// in rows of 128 bytes that two warps with neighbouring channels share (their 16-byte pieces
+// swapped as TMA's 128-byte swizzle does, which keeps both ways free of bank conflicts).
+// With kBulk one TMA store takes such a turn to Y while the next is written to the other
+// half of the buffer; what is less than 32 tokens of 64 channels, where a group or the
+// channels end, is stored by the lanes, 8 channels each (a TMA store writes past the end of
+// an odd row: its bounds are not those of single elements).
+constexpr int kTurnRow = 128, kTurnBytes = 32 * kTurnRow;
 
 template <typename Tout>
 struct Part;
@@ -190,8 +194,10 @@ struct Part<float> {
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
     }
-    // gx[j]: this lane's token 32 j + lane; y: the first token's row; ch0: the warp's first channel
-    __device__ void put(const float (&gx)[4], int n, float* y, int64_t ld, int64_t ch0, int64_t c_out, uint8_t*) {
+    // gx[j]: this lane's token 32 j + lane; y: the first token's row, number `row`; ch0: the warp's first channel
+    template <bool kBulk>
+    __device__ void put(const float (&gx)[4], int n, float* y, int64_t ld, int64_t ch0, int64_t c_out, uint8_t*, uint32_t&,
+                        const CUtensorMap*, int) {
         const int64_t ch = ch0 + (threadIdx.x & 31);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -219,14 +225,18 @@ struct Part<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo) * sl, __uint_as_float(hi) * sh);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    // turn: the buffer of two warps (kBulk: two turns); half: which half of it comes next
+    template <bool kBulk>
     __device__ void put(const float (&gx)[4], int n, __nv_bfloat16* y, int64_t ld, int64_t ch0, int64_t c_out,
-                        uint8_t* turn) {
-        const int lane = threadIdx.x & 31;
-        const uint32_t dst = smem_u32(turn) + (lane & 7) * kTurnRow + (((lane >> 3) ^ (lane >> 1)) & 3) * 16;
+                        uint8_t* turn, uint32_t& half, const CUtensorMap* ymap, int row) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int p0 = (warp & 1) * 4;  // the warp's first piece of a row
+        const uint32_t dst = smem_u32(turn) + (lane & 7) * kTurnRow + (((p0 + (lane >> 3)) ^ (lane & 7)) << 4);
         const int64_t ch = ch0 + 8 * (lane & 3);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 32 tokens
             if (32 * c >= n) break;
+            const uint32_t at = kBulk ? half * kTurnBytes : 0;
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 8 tokens
@@ -234,23 +244,34 @@ struct Part<__nv_bfloat16> {
                 const float s1 = __shfl_sync(0xFFFFFFFFu, gx[c], 8 * j + 2 * (lane & 3) + 1);
                 const uint32_t* a = r[2 * (c >> 1)] + 16 * (c & 1) + 4 * j;
                 const uint32_t* b = r[2 * (c >> 1) + 1] + 16 * (c & 1) + 4 * j;
-                stmatrix4_trans(dst + 8 * j * kTurnRow, pack(a[0], s0, a[1], s1), pack(a[2], s0, a[3], s1),
+                stmatrix4_trans(dst + at + 8 * j * kTurnRow, pack(a[0], s0, a[1], s1), pack(a[2], s0, a[3], s1),
                                 pack(b[0], s0, b[1], s1), pack(b[2], s0, b[3], s1));
+            }
+            if constexpr (kBulk) {
+                const bool leads = (warp & 1) == 0;
+                const bool whole = 32 * c + 32 <= n && ch0 - 8 * p0 + 64 <= c_out;
+                fence_proxy_async();
+                if (leads && elect_one()) tma_store_read<0>();  // the other half is free from here on
+                asm volatile("bar.sync %0, 64;" ::"r"(warp >> 1) : "memory");
+                if (whole && leads && elect_one())
+                    tma_store_2d(ymap, (int)ch0, row + 32 * c, smem_u32(turn) + at);
+                half ^= 1;
+                if (whole) continue;
             }
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int row = 8 * q + (lane >> 2);
-                const uint4 v = *reinterpret_cast<const uint4*>(turn + row * kTurnRow + (((lane & 3) ^ (row >> 1)) & 3) * 16);
-                if (32 * c + row >= n) continue;
-                __nv_bfloat16* to = y + (int64_t)(32 * c + row) * ld + ch;
+                const int i = 8 * q + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4*>(turn + at + i * kTurnRow + (((p0 + (lane & 3)) ^ (i & 7)) << 4));
+                if (32 * c + i >= n) continue;
+                __nv_bfloat16* to = y + (int64_t)(32 * c + i) * ld + ch;
                 if (ch + 8 <= c_out) {
                     *reinterpret_cast<uint4*>(to) = v;
                 } else {
                     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (ch + i < c_out) to[i] = __ushort_as_bfloat16((uint16_t)(u[i >> 1] >> (16 * (i & 1))));
+                    for (int e = 0; e < 8; ++e)
+                        if (ch + e < c_out) to[e] = __ushort_as_bfloat16((uint16_t)(u[e >> 1] >> (16 * (e & 1))));
                 }
             }
         }
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
-    Control& C = *reinterpret_cast<Control*>(turn_p + 4 * kTurnBytes);
+    Control& C = *reinterpret_cast<Control*>(turn_p + 2 * kTurnBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -470,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (!kSplit) {
         if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         const int q = warp & 3;  // the TMEM lanes that this warp can read
-        uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
+        uint8_t* turn = turn_p + ((warp - 2) >> 1) * kTurnBytes;
+        uint32_t half = 0;
         int acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
@@ -489,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&C.tempty[acc]));
             if (++acc == 2) { acc = 0; aphase ^= 1; }
-            part.put(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y, (int64_t)t.mt * kM + q * 32, p.c_out,
-                     turn);
+            part.template put<false>(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y,
+                                     (int64_t)t.mt * kM + q * 32, p.c_out, turn, half, nullptr, 0);
         }
         if (!ok) give_up(abort_flag);
     } else {
@@ -603,12 +625,13 @@ template <typename Tout>
 __global__ void __launch_bounds__(kPairThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
+                        const __grid_constant__ CUtensorMap ymap,
                         const ProdArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using S = Pair;
     uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
-    PairControl& C = *reinterpret_cast<PairControl*>(turn_p + 8 * kTurnBytes);
+    PairControl& C = *reinterpret_cast<PairControl*>(turn_p + 4 * 2 * kTurnBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -730,7 +753,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else {
         const int q = warp & 3;           // the TMEM lanes that this warp can read
         const int h = (warp - 2) >> 2;    // its half of the tokens
-        uint8_t* turn = turn_p + (warp - 2) * kTurnBytes;
+        uint8_t* turn = turn_p + ((warp - 2) >> 1) * 2 * kTurnBytes;
+        uint32_t half = 0;
         uint32_t aphase = 0;
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
@@ -752,9 +776,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // the values are in registers: no memory is handed over
             if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty), 0));
             aphase ^= 1;
-            part.put(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn);
+            part.template put<true>(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn,
+                                    half, &ymap, (int)t.row0 + c0);
         }
         if (!ok) give_up(abort_flag);
+        tma_store_wait();
     }
     fence_before();
     __syncthreads();
@@ -799,6 +825,17 @@ bool make_scale_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Y in bf16: boxes of 64 channels x 32 tokens, 128-byte swizzle.
+bool make_out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const ProdArgs& p) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.c_out, (cuuint64_t)p.n_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.ld_y * 2};
+    const cuuint32_t box[2] = {kTurnRow / 2, kTurnBytes / kTurnRow};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.Y, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kSplit, typename Tout, typename Tin = void>
 lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                          const ProdArgs& p, int parts, int sms, cudaStream_t st) {
@@ -814,7 +851,7 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     if (!ok) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const int64_t tiles = (p.offsets ? p.n_rows / kT + p.G : (p.n_rows + kT - 1) / kT) * p.mtiles;  // at most
     if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
-    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 4 * kTurnBytes + 1024 + sizeof(Control);
+    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 2 * kTurnBytes + 1024 + sizeof(Control);
     static_assert(smem <= 227 * 1024, "shared memory");
     auto kernel = product_kernel<kSplit, Tout, Tin>;
     static std::atomic<uint64_t> done{0};
@@ -849,7 +886,10 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
         !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kPairT / 2) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    constexpr size_t smem = (size_t)Pair::kStages * Pair::kStageBytes + 8 * kTurnBytes + 1024 + sizeof(PairControl);
+    CUtensorMap ymap = wmap;  // f32: not used
+    if (std::is_same_v<Tout, __nv_bfloat16> && !make_out_map(encode, &ymap, p))
+        return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    constexpr size_t smem = (size_t)Pair::kStages * Pair::kStageBytes + 4 * 2 * kTurnBytes + 1024 + sizeof(PairControl);
     static_assert(smem <= 227 * 1024, "shared memory");
     auto kernel = product_pair_kernel<Tout>;
     static std::atomic<uint64_t> done{0};
@@ -869,7 +909,7 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_pair_kernel launch");
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, ymap, p), "product_pair_kernel launch");
 }
 
 // Parts of c_in for the tiles of one matrix and at most 128 tokens: as many as SMs allow, in

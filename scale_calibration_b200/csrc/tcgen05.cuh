@@ -140,6 +140,21 @@ __device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&r)[32]) 
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+// A box of shared memory -> its place in a tensor (what lies past its ends is left out). The
+// thread that issued it waits for it: until at most kLeft copies still read shared memory, or
+// until all have arrived.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n"
+        " cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(src)
+        : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void tma_store_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Four 8 x 8 matrices of 16-bit values, stored transposed: thread i names the row of
 // matrix i / 8 that column i % 8 goes to.
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
