@@ -44,7 +44,8 @@ struct ProdArgs {
     int mtiles128;           // rows of scale tiles per matrix
     int stages_k;            // stages along c_in
     int steps;               // 64-column steps along c_in
-    int box;                 // tokens of one TMA copy (single CTAs): a tile brings the rows it has, rounded up to these
+    int box;                 // tokens of one TMA copy: a tile of a single CTA brings the rows it has, rounded up to these;
+                             // each CTA of a pair brings half of its tile's tokens in one
     const uint8_t* xs;       // scale tiles of the tokens
     const uint8_t* ws;       // scale tiles of the weights
     const float* xg;         // [n_rows]
@@ -88,8 +89,8 @@ struct Tile {
 
 // Walks over the tiles of all groups in order; every warp of the CTA does so by itself.
 // Groups are looked at 32 at a time, one per lane.
-template <int T>
 struct Walk {
+    int T;  // tokens of a tile
     int64_t g = 0;
     int64_t base = 0;  // tiles before group g
     __device__ void range(const ProdArgs& p, int64_t i, int64_t& lo, int64_t& hi) const {
@@ -113,7 +114,7 @@ struct Walk {
             int64_t lo = 0, hi = 0;
             if (g + lane < p.G) range(p, g + lane, lo, hi);
             // sums stop at 2^32 - 1: groups that overlap (decreasing offsets) can have more tiles
-            uint32_t inc = hi > lo ? (uint32_t)((hi - lo + T - 1) / T) * p.mtiles : 0;
+            uint32_t inc = hi > lo ? ((uint32_t)(hi - lo + T - 1) / (uint32_t)T) * p.mtiles : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // everything above overlaps the kernel before
     if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk<kT> walk;
+    Walk walk{kT};
     Tile t;
     if (warp == 0) {
         int stage = 0, ahead = 0;  // ahead: stages whose weights are on their way
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairRows = 192;     // rows per group from which groups are given to pairs
 
-constexpr int kPairT = 256;        // tokens of a pair's tile: two scale tiles
+constexpr int kPairT = 256;        // most tokens of a pair's tile: two scale tiles
 
 struct Pair {
     static constexpr int kA = kM * kRowBytes, kB = kPairT / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = 2 * 4 * kTileBytes;
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = C.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk<kPairT> walk;
+    Walk walk{2 * p.box};
     Tile t;
     if (warp == 0) {
         int stage = 0;
@@ -665,7 +666,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int64_t issued = 0;
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
-            const int half = ((t.rows + 15) & ~15) / 2;  // tokens that each CTA brings
+            const int half = ((t.rows + 15) & ~15) / 2;  // tokens of each CTA
+            const bool two = t.rows > kTileRows;         // scale tiles
+            const uint32_t bytes = 2 * (S::kA + p.box * kRowBytes + S::kSa + (two ? S::kSb : S::kSb / 2));  // of both CTAs
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * 2 * kM + rank * kM);
             const int xrow = (int)t.row0 + (int)rank * half;
             const int wsrow = (int)((t.g * p.mtiles128 + t.mt * 2 + rank) * p.steps);
@@ -676,13 +679,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (elect_one()) {
                     const uint32_t bar = cluster_addr(smem_u32(&C.full[stage]), 0);
                     const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
-                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), 2 * S::kStageBytes);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), bytes);
                     tma_load_2d_pair(a, &wmap, ks * kRowBytes, wrow, bar);
                     tma_load_2d_pair(b, &xmap, ks * kRowBytes, xrow, bar);
                     // past the last step or tile these bring other scales, or zeros, that no product uses
                     tma_load_2d_pair(sa, &wsmap, 0, wsrow + 4 * ks, bar);
                     tma_load_2d_pair(sb, &xsmap, 0, xsrow + 4 * ks, bar);
-                    tma_load_2d_pair(sb + 4 * kTileBytes, &xsmap, 0, xsrow + p.steps + 4 * ks, bar);
+                    if (two) tma_load_2d_pair(sb + 4 * kTileBytes, &xsmap, 0, xsrow + p.steps + 4 * ks, bar);
                 }
                 __syncwarp();
                 ++issued;
@@ -711,6 +714,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 fence_after();
                 const uint32_t n16 = (t.rows + 15) & ~15;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
+                const bool two = t.rows > kTileRows;
                 bool ready = false;
                 for (int ks = 0; ks < p.stages_k; ++ks) {
                     ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
@@ -728,7 +732,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         for (int k = 0; k < 4; ++k) {
                             if (k >= nk) break;
                             tmem_cp_scales_pair(cb + 8 * k, desc_sb + (at + k * (kTileBytes >> 4)));
-                            tmem_cp_scales_pair(cb + 8 * k + 4, desc_sb + (at + (4 + k) * (kTileBytes >> 4)));
+                            if (two)
+                                tmem_cp_scales_pair(cb + 8 * k + 4, desc_sb + (at + (4 + k) * (kTileBytes >> 4)));
                             tmem_cp_scales_pair(ca + 4 * k, desc_sa + (at + k * (kTileBytes >> 4)));
                             mma_nvfp4_pair(0, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 8 * k,
                                            (ks | k) ? 1u : 0u);
@@ -760,8 +765,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int64_t ch0 = (int64_t)t.mt * 2 * kM + rank * kM + q * 32;
             const float gw = __ldg(p.wg + t.g);
-            const int c0 = h * (kPairT / 2);
-            const int n = t.rows - c0 < kPairT / 2 ? t.rows - c0 : kPairT / 2;  // tokens of this warp, if above 0
+            const int c0 = h * p.box;
+            const int n = t.rows - c0 < p.box ? t.rows - c0 : p.box;  // tokens of this warp, if above 0
             float gx[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -877,13 +882,19 @@ template <typename Tout>
 lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                       ProdArgs p, int sms, cudaStream_t st) {
     p.mtiles = (p.mtiles128 + 1) / 2;
-    const int64_t tiles = (p.offsets ? p.n_rows / kPairT + p.G : (p.n_rows + kPairT - 1) / kPairT) * p.mtiles;
+    const int64_t pairs = sms / 2;
+    auto tiles_of = [&](int T) {  // at most
+        return (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;
+    };
+    auto rounds = [&](int T) { return (tiles_of(T) + pairs - 1) / pairs; };
+    p.box = !p.offsets && 7 * rounds(kPairT / 2) < 10 * rounds(kPairT) ? kPairT / 4 : kPairT / 2;
+    const int64_t tiles = tiles_of(2 * p.box);
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "too many tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, kPairT / 2) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, p.box) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     CUtensorMap ymap = wmap;  // f32: not used
@@ -895,7 +906,6 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
     static std::atomic<uint64_t> done{0};
     lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
-    const int64_t pairs = sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kPairThreads);
