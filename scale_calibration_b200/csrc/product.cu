@@ -44,8 +44,7 @@ struct ProdArgs {
     int mtiles128;           // rows of scale tiles per matrix
     int stages_k;            // stages along c_in
     int steps;               // 64-column steps along c_in
-    int box;                 // tokens of one TMA copy: a tile of a single CTA brings the rows it has, rounded up to these;
-                             // each CTA of a pair brings half of its tile's tokens in one
+    int box;                 // tokens of one TMA copy (single CTAs): a tile brings the rows it has, rounded up to these
     const uint8_t* xs;       // scale tiles of the tokens
     const uint8_t* ws;       // scale tiles of the weights
     const float* xg;         // [n_rows]
@@ -176,8 +175,8 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __fl
 // layout of mma fragments and turned by stmatrix through shared memory, 32 tokens at a time,
 // in rows of 128 bytes that two warps with neighbouring channels share (their 16-byte pieces
 // swapped as TMA's 128-byte swizzle does, which keeps both ways free of bank conflicts).
-// With kBulk one TMA store takes such a turn to Y while the next is written to the other
-// half of the buffer; what is less than 32 tokens of 64 channels, where a group or the
+// With a buffer of kTurns > 0 turns one TMA store takes each to Y (while the next is written to
+// the other half, if there are two); what is less than 32 tokens of 64 channels, where a group or the
 // channels end, is stored by the lanes, 8 channels each (a TMA store writes past the end of
 // an odd row: its bounds are not those of single elements).
 constexpr int kTurnRow = 128, kTurnBytes = 32 * kTurnRow;
@@ -196,7 +195,7 @@ struct Part<float> {
         for (int j = 0; j < 4; ++j) tmem_wait32(r[j]);
     }
     // gx[j]: this lane's token 32 j + lane; y: the first token's row, number `row`; ch0: the warp's first channel
-    template <bool kBulk>
+    template <int kTurns>
     __device__ void put(const float (&gx)[4], int n, float* y, int64_t ld, int64_t ch0, int64_t c_out, uint8_t*, uint32_t&,
                         const CUtensorMap*, int) {
         const int64_t ch = ch0 + (threadIdx.x & 31);
@@ -226,8 +225,8 @@ struct Part<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo) * sl, __uint_as_float(hi) * sh);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    // turn: the buffer of two warps (kBulk: two turns); half: which half of it comes next
-    template <bool kBulk>
+    // turn: the buffer of two warps; half: which half of it comes next
+    template <int kTurns>
     __device__ void put(const float (&gx)[4], int n, __nv_bfloat16* y, int64_t ld, int64_t ch0, int64_t c_out,
                         uint8_t* turn, uint32_t& half, const CUtensorMap* ymap, int row) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -237,7 +236,12 @@ struct Part<__nv_bfloat16> {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 32 tokens
             if (32 * c >= n) break;
-            const uint32_t at = kBulk ? half * kTurnBytes : 0;
+            const uint32_t at = kTurns == 2 ? half * kTurnBytes : 0;
+            const bool leads = (warp & 1) == 0;
+            if constexpr (kTurns == 1) {
+                if (leads && elect_one()) tma_store_read<0>();
+                asm volatile("bar.sync %0, 64;" ::"r"(warp >> 1) : "memory");
+            }
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 8 tokens
@@ -248,11 +252,10 @@ struct Part<__nv_bfloat16> {
                 stmatrix4_trans(dst + at + 8 * j * kTurnRow, pack(a[0], s0, a[1], s1), pack(a[2], s0, a[3], s1),
                                 pack(b[0], s0, b[1], s1), pack(b[2], s0, b[3], s1));
             }
-            if constexpr (kBulk) {
-                const bool leads = (warp & 1) == 0;
+            if constexpr (kTurns > 0) {
                 const bool whole = 32 * c + 32 <= n && ch0 - 8 * p0 + 64 <= c_out;
                 fence_proxy_async();
-                if (leads && elect_one()) tma_store_read<0>();  // the other half is free from here on
+                if (kTurns == 2 && leads && elect_one()) tma_store_read<0>();  // the other half is free from here on
                 asm volatile("bar.sync %0, 64;" ::"r"(warp >> 1) : "memory");
                 if (whole && leads && elect_one())
                     tma_store_2d(ymap, (int)ch0, row + 32 * c, smem_u32(turn) + at);
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&C.tempty[acc]));
             if (++acc == 2) { acc = 0; aphase ^= 1; }
-            part.template put<false>(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y,
+            part.template put<0>(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y,
                                      (int64_t)t.mt * kM + q * 32, p.c_out, turn, half, nullptr, 0);
         }
         if (!ok) give_up(abort_flag);
@@ -603,26 +606,28 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // the scales 96, which leaves no room for a second one: eight epilogue warps take a
 // whole accumulator into registers and free it before they scale and store.
 
-constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
+constexpr int kPairWarps = 8;      // of the epilogue
+constexpr int kPairThreads = 64 + 32 * kPairWarps;  // producer, MMA, epilogue
 constexpr int kPairRows = 192;     // rows per group from which groups are given to pairs
 
-constexpr int kPairT = 256;        // most tokens of a pair's tile: two scale tiles
-
+template <int T>  // tokens of a tile: 256 or 128
 struct Pair {
-    static constexpr int kA = kM * kRowBytes, kB = kPairT / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = 2 * 4 * kTileBytes;
+    static constexpr int kA = kM * kRowBytes, kB = T / 2 * kRowBytes, kSa = 4 * kTileBytes, kSb = T / kTileRows * 4 * kTileBytes;
     static constexpr int kStageBytes = kA + kB + kSa + kSb;
-    static constexpr int kStages = 5;
-    static constexpr int kScaleCol = kPairT, kSetCols = 16 + 32;
+    static constexpr int kStages = T == 256 ? 5 : 7;
+    static constexpr int kTurns = T == 256 ? 2 : 1;  // of each two epilogue warps
+    static constexpr int kScaleCol = T, kSetCols = 16 + 32;
     static_assert(kScaleCol + 2 * kSetCols <= 512, "TMEM columns");
+    static constexpr int kTurnTotal = kPairWarps / 2 * kTurns * kTurnBytes;
 };
 
 struct PairControl {
-    uint64_t full[Pair::kStages], empty[Pair::kStages], tfull, tempty, done;
+    uint64_t full[Pair<128>::kStages], empty[Pair<128>::kStages], tfull, tempty, done;
     uint32_t tmem;
     int abort_flag;
 };
 
-template <typename Tout>
+template <int T, typename Tout>
 __global__ void __launch_bounds__(kPairThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
@@ -630,9 +635,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const ProdArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    using S = Pair;
+    using S = Pair<T>;
     uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
-    PairControl& C = *reinterpret_cast<PairControl*>(turn_p + 4 * 2 * kTurnBytes);
+    PairControl& C = *reinterpret_cast<PairControl*>(turn_p + S::kTurnTotal);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = C.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk walk{2 * p.box};
+    Walk walk{T};
     Tile t;
     if (warp == 0) {
         int stage = 0;
@@ -667,8 +672,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int half = ((t.rows + 15) & ~15) / 2;  // tokens of each CTA
-            const bool two = t.rows > kTileRows;         // scale tiles
-            const uint32_t bytes = 2 * (S::kA + p.box * kRowBytes + S::kSa + (two ? S::kSb : S::kSb / 2));  // of both CTAs
+            const bool two = T > kTileRows && t.rows > kTileRows;         // scale tiles
+            const uint32_t bytes = 2 * (S::kA + S::kB + S::kSa + (two ? 2 : 1) * 4 * kTileBytes);  // of both CTAs
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * 2 * kM + rank * kM);
             const int xrow = (int)t.row0 + (int)rank * half;
             const int wsrow = (int)((t.g * p.mtiles128 + t.mt * 2 + rank) * p.steps);
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 fence_after();
                 const uint32_t n16 = (t.rows + 15) & ~15;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
-                const bool two = t.rows > kTileRows;
+                const bool two = T > kTileRows && t.rows > kTileRows;
                 bool ready = false;
                 for (int ks = 0; ks < p.stages_k; ++ks) {
                     ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
@@ -758,15 +763,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else {
         const int q = warp & 3;           // the TMEM lanes that this warp can read
         const int h = (warp - 2) >> 2;    // its half of the tokens
-        uint8_t* turn = turn_p + ((warp - 2) >> 1) * 2 * kTurnBytes;
+        uint8_t* turn = turn_p + ((warp - 2) >> 1) * S::kTurns * kTurnBytes;
         uint32_t half = 0;
         uint32_t aphase = 0;
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int64_t ch0 = (int64_t)t.mt * 2 * kM + rank * kM + q * 32;
             const float gw = __ldg(p.wg + t.g);
-            const int c0 = h * p.box;
-            const int n = t.rows - c0 < p.box ? t.rows - c0 : p.box;  // tokens of this warp, if above 0
+            const int c0 = h * (T / 2);
+            const int n = t.rows - c0 < T / 2 ? t.rows - c0 : T / 2;  // tokens of this warp, if above 0
             float gx[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -781,7 +786,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // the values are in registers: no memory is handed over
             if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&C.tempty), 0));
             aphase ^= 1;
-            part.template put<true>(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn,
+            part.template put<S::kTurns>(gx, n, static_cast<Tout*>(p.Y) + (t.row0 + c0) * p.ld_y, p.ld_y, ch0, p.c_out, turn,
                                     half, &ymap, (int)t.row0 + c0);
         }
         if (!ok) give_up(abort_flag);
@@ -878,31 +883,30 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_kernel launch");
 }
 
-template <typename Tout>
+int64_t pair_tiles(const ProdArgs& p, int T) {  // at most
+    return (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * ((p.mtiles128 + 1) / 2);
+}
+
+template <int T, typename Tout>
 lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                       ProdArgs p, int sms, cudaStream_t st) {
+    using S = Pair<T>;
     p.mtiles = (p.mtiles128 + 1) / 2;
-    const int64_t pairs = sms / 2;
-    auto tiles_of = [&](int T) {  // at most
-        return (p.offsets ? p.n_rows / T + p.G : (p.n_rows + T - 1) / T) * p.mtiles;
-    };
-    auto rounds = [&](int T) { return (tiles_of(T) + pairs - 1) / pairs; };
-    p.box = !p.offsets && 7 * rounds(kPairT / 2) < 10 * rounds(kPairT) ? kPairT / 4 : kPairT / 2;
-    const int64_t tiles = tiles_of(2 * p.box);
+    const int64_t pairs = sms / 2, tiles = pair_tiles(p, T);
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "too many tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, p.box) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T / 2) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     CUtensorMap ymap = wmap;  // f32: not used
     if (std::is_same_v<Tout, __nv_bfloat16> && !make_out_map(encode, &ymap, p))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    constexpr size_t smem = (size_t)Pair::kStages * Pair::kStageBytes + 4 * 2 * kTurnBytes + 1024 + sizeof(PairControl);
+    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + S::kTurnTotal + 1024 + sizeof(PairControl);
     static_assert(smem <= 227 * 1024, "shared memory");
-    auto kernel = product_pair_kernel<Tout>;
+    auto kernel = product_pair_kernel<T, Tout>;
     static std::atomic<uint64_t> done{0};
     lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
@@ -941,8 +945,12 @@ int split_parts(const ProdArgs& p, int sms) {
 template <typename Tout>
 lh_status dispatch(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                    const ProdArgs& p, int sms, cudaStream_t st) {
-    if (p.offsets ? p.n_rows >= kPairRows * p.G : p.n_rows > kT)
-        return launch_pair<Tout>(encode, X, W, c_in, p, sms, st);
+    if (p.offsets ? p.n_rows >= kPairRows * p.G : p.n_rows > kT) {
+        const int64_t pairs = sms / 2;
+        auto rounds = [&](int T) { return (pair_tiles(p, T) + pairs - 1) / pairs; };
+        if (!p.offsets && 7 * rounds(128) < 10 * rounds(256)) return launch_pair<128, Tout>(encode, X, W, c_in, p, sms, st);
+        return launch_pair<256, Tout>(encode, X, W, c_in, p, sms, st);
+    }
     if (!p.offsets) {
         const int parts = split_parts(p, sms);
         if (parts > 1) return launch_product<true, Tout>(encode, X, W, c_in, p, parts, sms, st);
