@@ -144,22 +144,21 @@ struct Walk {
     }
 };
 
-// Waits for the phase of `parity` with one answer for the warp; false after 1 s, or when
-// another warp gave up. The timer is read only after many tries: reading it takes longer
-// than most waits.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+// Waits for the phase of `parity`; false after 1 s, or when another warp gave up. The timer
+// is read only after many tries: reading it takes longer than most waits.
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     uint64_t t0 = 0;
-    bool ok = true;
     for (uint32_t it = 1; !mbar_try(bar, parity); ++it) {
         if ((it & 255) != 0) continue;
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
-        if (*abort_flag || now - t0 > kTimeoutNs) {
-            ok = false;
-            break;
-        }
+        if (*abort_flag || now - t0 > kTimeoutNs) return false;
     }
-    return __all_sync(0xFFFFFFFFu, ok);
+    return true;
+}
+// The same with one answer for the warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity, abort_flag));
 }
 __device__ __forceinline__ void give_up(volatile int* flag) {
     *flag = 1;
@@ -456,18 +455,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
             const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
             const uint32_t d = acc * kT;
-            bool ready = false;
-            for (int ks = ks0; ks < ks1; ++ks) {
-                ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
-                if (!ok) break;
-                fence_after();
-                // a first look at the next stage, answered while this one's products are issued
-                const bool last = stage + 1 == S::kStages;
-                const bool seen = mbar_test(smem_u32(&C.full[last ? 0 : stage + 1]), last ? phase ^ 1 : phase);
-                if (elect_one()) {
+            // One lane runs the whole row: its own instructions bound a short stage, and a choice
+            // of lane and an answer for the warp at every stage would add a third to them.
+            if (elect_one()) {
+                bool ready = false;
+                int st = stage;
+                uint32_t ph = phase, se = set;
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!ready && !lane_wait(smem_u32(&C.full[st]), ph, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
                     const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                    const uint32_t at = stage * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
-                    const uint32_t ca = S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                    const uint32_t at = st * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
+                    const uint32_t ca = S::kScaleCol + se * S::kSetCols, cb = ca + 16, bar = smem_u32(&C.empty[st]);
+                    if (++st == S::kStages) { st = 0; ph ^= 1; }
+                    se ^= 1;
+                    // a first look at the next stage, answered while this one's products are issued
+                    ready = mbar_test(smem_u32(&C.full[st]), ph);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k >= nk) break;
@@ -476,13 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         mma_nvfp4(d, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 4 * k,
                                   (ks > ks0 || k > 0) ? 1u : 0u);
                     }
-                    mma_commit(smem_u32(&C.empty[stage]));
-                    if (ks == ks1 - 1) mma_commit(smem_u32(&C.tfull[acc]));
+                    mma_commit(bar);
                 }
-                ready = __all_sync(0xFFFFFFFFu, seen);
-                set ^= 1;
-                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+                if (ok) mma_commit(smem_u32(&C.tfull[acc]));
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            stage += ks1 - ks0;
+            phase ^= (stage / S::kStages) & 1;
+            stage %= S::kStages;
+            set ^= (ks1 - ks0) & 1;
             if (++acc == 2) { acc = 0; aphase ^= 1; }
         }
         if (!ok) {  // the products in flight end before the CTA does
@@ -720,18 +728,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const uint32_t n16 = (t.rows + 15) & ~15;
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | (2u << 27);  // M = 256
                 const bool two = T > kTileRows && t.rows > kTileRows;
-                bool ready = false;
-                for (int ks = 0; ks < p.stages_k; ++ks) {
-                    ok = ready || warp_wait(smem_u32(&C.full[stage]), phase, abort_flag);
-                    if (!ok) break;
-                    fence_after();
-                    // a first look at the next stage, answered while this one's products are issued
-                    const bool last = stage + 1 == S::kStages;
-                    const bool seen = mbar_test(smem_u32(&C.full[last ? 0 : stage + 1]), last ? phase ^ 1 : phase);
-                    if (elect_one()) {
+                if (elect_one()) {  // one lane runs the whole row, as above
+                    bool ready = false;
+                    int st = stage;
+                    uint32_t ph = phase, se = set;
+                    for (int ks = 0; ks < p.stages_k; ++ks) {
+                        if (!ready && !lane_wait(smem_u32(&C.full[st]), ph, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
                         const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                        const uint32_t at = stage * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
-                        const uint32_t ca = S::kScaleCol + set * S::kSetCols, cb = ca + 16;
+                        const uint32_t at = st * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
+                        const uint32_t ca = S::kScaleCol + se * S::kSetCols, cb = ca + 16, bar = smem_u32(&C.empty[st]);
+                        if (++st == S::kStages) { st = 0; ph ^= 1; }
+                        se ^= 1;
+                        ready = mbar_test(smem_u32(&C.full[st]), ph);
                         // step by step: the copies of a step run beside the products of the one before
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -743,13 +755,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             mma_nvfp4_pair(0, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 8 * k,
                                            (ks | k) ? 1u : 0u);
                         }
-                        mma_commit_pair(smem_u32(&C.empty[stage]));
-                        if (ks == p.stages_k - 1) mma_commit_pair(smem_u32(&C.tfull));
+                        mma_commit_pair(bar);
                     }
-                    ready = __all_sync(0xFFFFFFFFu, seen);
-                    set ^= 1;
-                    if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+                    if (ok) mma_commit_pair(smem_u32(&C.tfull));
                 }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                stage += p.stages_k;
+                phase ^= (stage / S::kStages) & 1;
+                stage %= S::kStages;
+                set ^= p.stages_k & 1;
                 aphase ^= 1;
             }
             if (!ok) {  // the products in flight end before the CTAs do
