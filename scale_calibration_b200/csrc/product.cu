@@ -414,23 +414,30 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 __syncwarp();
                 asm volatile("griddepcontrol.wait;" ::: "memory");
             }
-            for (int ks = ks0; ks < ks1; ++ks) {
-                ok = warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
-                if (!ok) break;
-                if (elect_one()) {
-                    const uint32_t bar = smem_u32(&C.full[stage]), b = ring + stage * S::kStageBytes + S::kA;
-                    if (ahead == 0) weights(stage, ks);
+            int n = 0;           // stages of this tile
+            if (elect_one()) {  // one lane for all of them
+                int st = stage;
+                uint32_t ph = phase;
+                for (int ks = ks0; ks < ks1; ++ks, ++n) {
+                    ok = lane_wait(smem_u32(&C.empty[st]), ph ^ 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&C.full[st]), b = ring + st * S::kStageBytes + S::kA;
+                    if (n >= ahead) weights(st, ks);
                     if constexpr (!kFused) {
                         for (int i = 0; i < boxes; ++i)
                             tma_load_2d(b + i * p.box * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * p.box, bar);
                         tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
                     }
+                    if (++st == S::kStages) { st = 0; ph ^= 1; }
                 }
-                __syncwarp();
-                if (ahead > 0) --ahead;
-                ++issued;
-                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            n = __reduce_max_sync(0xFFFFFFFFu, n);
+            ahead = 0;
+            issued += n;
+            stage += n;
+            phase ^= (stage / S::kStages) & 1;
+            stage %= S::kStages;
         }
         if (!ok) {  // the loads in flight land before the CTA ends
             give_up(abort_flag);
@@ -669,41 +676,63 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_meet();  // the barriers of both CTAs are ready
     fence_after();
     const uint32_t tmem = C.tmem;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // everything above overlaps the kernel before
+    if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     Walk walk{T};
     Tile t;
     if (warp == 0) {
-        int stage = 0;
+        int stage = 0, ahead = 0;  // ahead: stages whose weights are on their way
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
             const int half = ((t.rows + 15) & ~15) / 2;  // tokens of each CTA
-            const bool two = T > kTileRows && t.rows > kTileRows;         // scale tiles
-            const uint32_t bytes = 2 * (S::kA + S::kB + S::kSa + (two ? 2 : 1) * 4 * kTileBytes);  // of both CTAs
+            const int boxes = (half + p.box - 1) / p.box;
+            const bool two = T > kTileRows && t.rows > kTileRows;  // scale tiles
+            const uint32_t bytes = 2 * (S::kA + boxes * p.box * kRowBytes + S::kSa + (two ? 2 : 1) * 4 * kTileBytes);  // both CTAs
             const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * 2 * kM + rank * kM);
             const int xrow = (int)t.row0 + (int)rank * half;
             const int wsrow = (int)((t.g * p.mtiles128 + t.mt * 2 + rank) * p.steps);
             const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
-            for (int ks = 0; ks < p.stages_k; ++ks) {
-                ok = warp_wait(smem_u32(&C.empty[stage]), phase ^ 1, abort_flag);
-                if (!ok) break;
-                if (elect_one()) {
-                    const uint32_t bar = cluster_addr(smem_u32(&C.full[stage]), 0);
-                    const uint32_t a = ring + stage * S::kStageBytes, b = a + S::kA, sa = b + S::kB, sb = sa + S::kSa;
-                    if (rank == 0) mbar_expect_tx(smem_u32(&C.full[stage]), bytes);
-                    tma_load_2d_pair(a, &wmap, ks * kRowBytes, wrow, bar);
-                    tma_load_2d_pair(b, &xmap, ks * kRowBytes, xrow, bar);
-                    // past the last step or tile these bring other scales, or zeros, that no product uses
-                    tma_load_2d_pair(sa, &wsmap, 0, wsrow + 4 * ks, bar);
+            auto weights = [&](int s, int ks) {
+                const uint32_t bar = cluster_addr(smem_u32(&C.full[s]), 0), a = ring + s * S::kStageBytes;
+                if (rank == 0) mbar_expect_tx(smem_u32(&C.full[s]), bytes);
+                tma_load_2d_pair(a, &wmap, ks * kRowBytes, wrow, bar);
+                // past the last step or tile these bring other scales, or zeros, that no product uses
+                tma_load_2d_pair(a + S::kA + S::kB, &wsmap, 0, wsrow + 4 * ks, bar);
+            };
+            if (p.early && u == first) {
+                ahead = p.stages_k < S::kStages ? p.stages_k : S::kStages;
+                if (elect_one())
+                    for (int i = 0; i < ahead; ++i) weights(i, i);
+                __syncwarp();
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            }
+            int n = 0;           // stages of this tile
+            if (elect_one()) {  // one lane for all of them
+                int st = stage;
+                uint32_t ph = phase;
+                for (int ks = 0; ks < p.stages_k; ++ks, ++n) {
+                    ok = lane_wait(smem_u32(&C.empty[st]), ph ^ 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t bar = cluster_addr(smem_u32(&C.full[st]), 0);
+                    const uint32_t b = ring + st * S::kStageBytes + S::kA, sb = b + S::kB + S::kSa;
+                    if (n >= ahead) weights(st, ks);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d_pair(b + i * p.box * kRowBytes, &xmap, ks * kRowBytes, xrow + i * p.box, bar);
                     tma_load_2d_pair(sb, &xsmap, 0, xsrow + 4 * ks, bar);
                     if (two) tma_load_2d_pair(sb + 4 * kTileBytes, &xsmap, 0, xsrow + p.steps + 4 * ks, bar);
+                    if (++st == S::kStages) { st = 0; ph ^= 1; }
                 }
-                __syncwarp();
-                ++issued;
-                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            n = __reduce_max_sync(0xFFFFFFFFu, n);
+            ahead = 0;
+            issued += n;
+            stage += n;
+            phase ^= (stage / S::kStages) & 1;
+            stage %= S::kStages;
         }
         if (!ok) {  // the loads in flight land before the CTAs end (both report to the first one's barriers)
             give_up(abort_flag);
@@ -779,6 +808,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int h = (warp - 2) >> 2;    // its half of the tokens
         uint8_t* turn = turn_p + ((warp - 2) >> 1) * S::kTurns * kTurnBytes;
         uint32_t half = 0;
+        if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t aphase = 0;
         bool ok = true;
         for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
@@ -906,13 +936,17 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
                       ProdArgs p, int sms, cudaStream_t st) {
     using S = Pair<T>;
     p.mtiles = (p.mtiles128 + 1) / 2;
+    // the power of 2 that takes half of a group of average size in one copy (a copy costs its
+    // rows, used or not, about 1.3 ns each)
+    p.box = 8;
+    while (p.box < T / 2 && 2 * p.box * p.G < p.n_rows) p.box *= 2;
     const int64_t pairs = sms / 2, tiles = pair_tiles(p, T);
     const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
     if (tiles > INT_MAX || xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "too many tiles");
     CUtensorMap wmap, xmap, wsmap, xsmap;
     if (!make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) ||
-        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, T / 2) ||
+        !make_map(encode, &xmap, X, p.n_rows, c_in / 2, p.box) ||
         !make_scale_map(encode, &wsmap, p.ws, ws_tiles) || !make_scale_map(encode, &xsmap, p.xs, xs_tiles))
         return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     CUtensorMap ymap = wmap;  // f32: not used
