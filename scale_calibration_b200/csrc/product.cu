@@ -6,10 +6,11 @@
 // matrix and all tokens), with E2M1 values q, E4M3 block scales v and FP32 global
 // scales g: W4A4 inference with the weights that lh_quantize_nvfp4 exports.
 //
-// One warp-specialised CTA per SM walks over output tiles of 128 channels x T tokens:
-// warp 0 fills a ring of stages by TMA (128 bytes = 256 values of each row, and the
-// scale tiles of those columns), warp 1 copies the scales to TMEM and issues
-// tcgen05.mma kind::mxf4nvf4 (K = 64 a step), four warps read the accumulators and
+// Two kernels, both with one warp-specialised CTA per SM: pairs of CTAs that walk over tiles of
+// 256 channels x up to 256 tokens, and, for few tiles of few tokens, clusters of CTAs that
+// share the columns of one tile. Warp 0 fills a ring of stages by TMA (128 bytes = 256 values
+// of each row, and the scale tiles of those columns), warp 1 copies the scales to TMEM and
+// issues tcgen05.mma kind::mxf4nvf4 (K = 64 a step), the others read the accumulators and
 // store. Channels are the M side, so the N side, the tokens, can be cut to the 16
 // rows that a ragged group's last tile needs.
 #include <climits>
@@ -44,7 +45,7 @@ struct ProdArgs {
     int mtiles128;           // rows of scale tiles per matrix
     int stages_k;            // stages along c_in
     int steps;               // 64-column steps along c_in
-    int box;                 // tokens of one TMA copy (single CTAs): a tile brings the rows it has, rounded up to these
+    int box;                 // tokens of one TMA copy: a tile of a pair brings the rows it has, rounded up to these
     const uint8_t* xs;       // scale tiles of the tokens
     const uint8_t* ws;       // scale tiles of the weights
     const float* xg;         // [n_rows]
@@ -64,9 +65,9 @@ struct Shape {
     static constexpr int kA = kM * kRowBytes, kB = kT * kRowBytes, kSa = 4 * kTileBytes, kSb = 4 * kTileBytes;
     static constexpr int kStageBytes = kA + kB + kSa + kSb;
     static constexpr int kStages = 6;
-    // TMEM: two accumulators, then the scales of two stages (addresses of scales are
+    // TMEM: the accumulator, then the scales of two stages (addresses of scales are
     // multiples of 4 columns, so a tile starts with a scale tile)
-    static constexpr int kScaleCol = 2 * kT, kSetCols = 32, kTmemCols = 512;  // all
+    static constexpr int kScaleCol = kT, kSetCols = 32, kTmemCols = 512;  // all
     static_assert(kScaleCol + 2 * kSetCols <= kTmemCols, "TMEM columns");
     static_assert(kStages * kStageBytes >= 2 * kT * kM * 4, "split: the partial sums reuse the ring");
 };
@@ -76,7 +77,7 @@ constexpr int kFewTokens = 8;  // most tokens that the product quantises itself
 struct Control {
     uint32_t amax[4][kFewTokens];  // of the tokens, by warp
     float gscale[kFewTokens];
-    uint64_t full[Shape::kStages], empty[Shape::kStages], tfull[2], tempty[2], done, sums;
+    uint64_t full[Shape::kStages], empty[Shape::kStages], tfull, done, sums;
     uint32_t tmem;
     int abort_flag;
 };
@@ -174,8 +175,8 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* y, float v) { *y = __fl
 // layout of mma fragments and turned by stmatrix through shared memory, 32 tokens at a time,
 // in rows of 128 bytes that two warps with neighbouring channels share (their 16-byte pieces
 // swapped as TMA's 128-byte swizzle does, which keeps both ways free of bank conflicts).
-// With a buffer of kTurns > 0 turns one TMA store takes each to Y (while the next is written to
-// the other half, if there are two); what is less than 32 tokens of 64 channels, where a group or the
+// One TMA store takes each turn to Y, while the next is written to the other half of the buffer if
+// it holds two (kTurns); what is less than 32 tokens of 64 channels, where a group or the
 // channels end, is stored by the lanes, 8 channels each (a TMA store writes past the end of
 // an odd row: its bounds are not those of single elements).
 constexpr int kTurnRow = 128, kTurnBytes = 32 * kTurnRow;
@@ -251,16 +252,14 @@ struct Part<__nv_bfloat16> {
                 stmatrix4_trans(dst + at + 8 * j * kTurnRow, pack(a[0], s0, a[1], s1), pack(a[2], s0, a[3], s1),
                                 pack(b[0], s0, b[1], s1), pack(b[2], s0, b[3], s1));
             }
-            if constexpr (kTurns > 0) {
-                const bool whole = 32 * c + 32 <= n && ch0 - 8 * p0 + 64 <= c_out;
-                fence_proxy_async();
-                if (kTurns == 2 && leads && elect_one()) tma_store_read<0>();  // the other half is free from here on
-                asm volatile("bar.sync %0, 64;" ::"r"(warp >> 1) : "memory");
-                if (whole && leads && elect_one())
-                    tma_store_2d(ymap, (int)ch0, row + 32 * c, smem_u32(turn) + at);
-                half ^= 1;
-                if (whole) continue;
-            }
+            const bool whole = 32 * c + 32 <= n && ch0 - 8 * p0 + 64 <= c_out;
+            fence_proxy_async();
+            if (kTurns == 2 && leads && elect_one()) tma_store_read<0>();  // the other half is free from here on
+            asm volatile("bar.sync %0, 64;" ::"r"(warp >> 1) : "memory");
+            if (whole && leads && elect_one())
+                tma_store_2d(ymap, (int)ch0, row + 32 * c, smem_u32(turn) + at);
+            half ^= 1;
+            if (whole) continue;
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -337,32 +336,32 @@ __device__ void write_tokens(const ProdArgs& p, Control& C, uint32_t ring, int k
     asm volatile("bar.sync 1, 128;" ::: "memory");  // the scales are there for all
 }
 
-// kSplit: a cluster of CTAs works on one tile, each on a part of c_in; the partial sums
-// meet in distributed shared memory, each CTA adding up those of its share of the tokens in the
-// order of the parts (the same sums every time). Without it a CTA walks over whole tiles.
+// ---------------------------------------------------------------- few tiles of few tokens
 //
-// Tin: with few tokens of type Tin instead of quantised ones (kSplit only), every CTA
+// A cluster of CTAs works on one tile of 128 channels and all tokens (at most 128), each on
+// a part of c_in; the partial sums meet in distributed shared memory, each CTA adding up
+// those of its share of the tokens in the order of the parts (the same sums every time).
+//
+// Tin: with few tokens of type Tin instead of quantised ones, every CTA
 // quantises its part of them: the epilogue warps, idle until the sums are ready, take each
 // token's largest |x| and write the codes and scales of a stage where TMA would put them,
 // while the weights are on their way, in one launch instead of two.
-template <bool kSplit, typename Tout, typename Tin = void>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                              const __grid_constant__ CUtensorMap xmap,
-                                                              const __grid_constant__ CUtensorMap wsmap,
-                                                              const __grid_constant__ CUtensorMap xsmap,
-                                                              const ProdArgs p) {
+template <typename Tout, typename Tin = void>
+__global__ void __launch_bounds__(kThreads, 1) product_split_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                    const __grid_constant__ CUtensorMap xmap,
+                                                                    const __grid_constant__ CUtensorMap wsmap,
+                                                                    const __grid_constant__ CUtensorMap xsmap,
+                                                                    const ProdArgs p) {
     using S = Shape;
     constexpr bool kFused = !std::is_void_v<Tin>;
-    static_assert(kSplit || !kFused, "few tokens make few tiles");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base_p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* turn_p = base_p + S::kStages * S::kStageBytes;  // the epilogue warps' rows
-    Control& C = *reinterpret_cast<Control*>(turn_p + 2 * kTurnBytes);
+    Control& C = *reinterpret_cast<Control*>(base_p + S::kStages * S::kStageBytes);
     const uint32_t ring = smem_u32(base_p);
     volatile int* abort_flag = &C.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = kSplit ? (int)cluster_size() : 1, rank = kSplit ? (int)cluster_rank() : 0;
-    const int first = blockIdx.x / parts, step = gridDim.x / parts;
+    const int parts = (int)cluster_size(), rank = (int)cluster_rank();
+    const int mt = blockIdx.x / parts, rows = (int)p.n_rows;
     const int ks0 = p.stages_k * rank / parts, ks1 = p.stages_k * (rank + 1) / parts;
 
     if (threadIdx.x == 0) {
@@ -370,10 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             mbar_init(smem_u32(&C.full[s]), kFused ? 5 : 1);  // TMA, and the warps that quantise
             mbar_init(smem_u32(&C.empty[s]), 1);
         }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(smem_u32(&C.tfull[a]), 1);
-            mbar_init(smem_u32(&C.tempty[a]), 4);
-        }
+        mbar_init(smem_u32(&C.tfull), 1);
         mbar_init(smem_u32(&C.done), 1);
         mbar_init(smem_u32(&C.sums), 1);
         C.abort_flag = 0;
@@ -387,119 +383,85 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // everything above overlaps the kernel before
     if (!p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Walk walk{kT};
-    Tile t;
     if (warp == 0) {
-        int stage = 0, ahead = 0;  // ahead: stages whose weights are on their way
-        uint32_t phase = 0;
-        int64_t issued = 0;
+        int n = 0;  // stages on their way
         bool ok = true;
-        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
-            const int wrow = (int)(t.g * p.c_out + (int64_t)t.mt * kM);
-            const int wsrow = (int)((t.g * p.mtiles + t.mt) * p.steps);
-            const int xsrow = (int)((group_tile(t.lo, t.g) + t.sub / kTileRows) * p.steps);
-            const int boxes = (t.rows + p.box - 1) / p.box;
-            const uint32_t bytes = S::kA + S::kSa + (kFused ? 0 : boxes * p.box * kRowBytes + S::kSb);
+        if (elect_one()) {  // one lane for all of them
+            const uint32_t bytes = S::kA + S::kSa + (kFused ? 0 : p.box * kRowBytes + S::kSb);
             auto weights = [&](int s, int ks) {
                 const uint32_t bar = smem_u32(&C.full[s]), a = ring + s * S::kStageBytes;
                 mbar_expect_tx(bar, bytes);
-                tma_load_2d(a, &wmap, ks * kRowBytes, wrow, bar);
+                tma_load_2d(a, &wmap, ks * kRowBytes, mt * kM, bar);
                 // past the last step this brings other scales, or zeros, that no product uses
-                tma_load_2d(a + S::kA + S::kB, &wsmap, 0, wsrow + 4 * ks, bar);
+                tma_load_2d(a + S::kA + S::kB, &wsmap, 0, mt * p.steps + 4 * ks, bar);
             };
-            if (p.early && u == first) {
-                ahead = ks1 - ks0 < S::kStages ? ks1 - ks0 : S::kStages;
-                if (elect_one())
-                    for (int i = 0; i < ahead; ++i) weights(i, ks0 + i);
-                __syncwarp();
+            int ahead = 0;  // stages whose weights are on their way
+            if (p.early) {
+                for (; ahead < ks1 - ks0 && ahead < S::kStages; ++ahead) weights(ahead, ks0 + ahead);
                 asm volatile("griddepcontrol.wait;" ::: "memory");
             }
-            int n = 0;           // stages of this tile
-            if (elect_one()) {  // one lane for all of them
-                int st = stage;
-                uint32_t ph = phase;
-                for (int ks = ks0; ks < ks1; ++ks, ++n) {
-                    ok = lane_wait(smem_u32(&C.empty[st]), ph ^ 1, abort_flag);
-                    if (!ok) break;
+            int st = 0;
+            uint32_t ph = 0;
+            for (int ks = ks0; ks < ks1; ++ks, ++n) {
+                ok = lane_wait(smem_u32(&C.empty[st]), ph ^ 1, abort_flag);
+                if (!ok) break;
+                if (n >= ahead) weights(st, ks);
+                if constexpr (!kFused) {
                     const uint32_t bar = smem_u32(&C.full[st]), b = ring + st * S::kStageBytes + S::kA;
-                    if (n >= ahead) weights(st, ks);
-                    if constexpr (!kFused) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(b + i * p.box * kRowBytes, &xmap, ks * kRowBytes, (int)t.row0 + i * p.box, bar);
-                        tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, xsrow + 4 * ks, bar);
-                    }
-                    if (++st == S::kStages) { st = 0; ph ^= 1; }
+                    tma_load_2d(b, &xmap, ks * kRowBytes, 0, bar);
+                    tma_load_2d(b + S::kB + S::kSa, &xsmap, 0, 4 * ks, bar);
                 }
+                if (++st == S::kStages) { st = 0; ph ^= 1; }
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            n = __reduce_max_sync(0xFFFFFFFFu, n);
-            ahead = 0;
-            issued += n;
-            stage += n;
-            phase ^= (stage / S::kStages) & 1;
-            stage %= S::kStages;
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        n = __reduce_max_sync(0xFFFFFFFFu, n);
         if (!ok) {  // the loads in flight land before the CTA ends
             give_up(abort_flag);
-            const int n = issued < S::kStages ? (int)issued : S::kStages;
-            for (int i = 0; i < n; ++i) {
-                if (--stage < 0) { stage = S::kStages - 1; phase ^= 1; }
+            for (int i = n < S::kStages ? 0 : n - S::kStages; i < n; ++i) {
                 int none = 0;
-                warp_wait(smem_u32(&C.full[stage]), phase, &none);
+                warp_wait(smem_u32(&C.full[i % S::kStages]), (i / S::kStages) & 1, &none);
             }
         }
     } else if (warp == 1) {
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, aphase = 0, set = 0;
         bool ok = true;
         const uint64_t desc_a = desc_k_sw128(ring), desc_b = desc_k_sw128(ring + S::kA);
         const uint64_t desc_sa = desc_scales(ring + S::kA + S::kB), desc_sb = desc_scales(ring + S::kA + S::kB + S::kSa);
-        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
-            ok = warp_wait(smem_u32(&C.tempty[acc]), aphase ^ 1, abort_flag);
-            if (!ok) break;
-            fence_after();
-            const uint32_t n16 = (t.rows + 15) & ~15;
-            // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
-            const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
-            const uint32_t d = acc * kT;
-            // One lane runs the whole row: its own instructions bound a short stage, and a choice
-            // of lane and an answer for the warp at every stage would add a third to them.
-            if (elect_one()) {
-                bool ready = false;
-                int st = stage;
-                uint32_t ph = phase, se = set;
-                for (int ks = ks0; ks < ks1; ++ks) {
-                    if (!ready && !lane_wait(smem_u32(&C.full[st]), ph, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
-                    const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
-                    const uint32_t at = st * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
-                    const uint32_t ca = S::kScaleCol + se * S::kSetCols, cb = ca + 16, bar = smem_u32(&C.empty[st]);
-                    if (++st == S::kStages) { st = 0; ph ^= 1; }
-                    se ^= 1;
-                    // a first look at the next stage, answered while this one's products are issued
-                    ready = mbar_test(smem_u32(&C.full[st]), ph);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= nk) break;
-                        tmem_cp_scales(cb + 4 * k, desc_sb + (at + k * (kTileBytes >> 4)));
-                        tmem_cp_scales(ca + 4 * k, desc_sa + (at + k * (kTileBytes >> 4)));
-                        mma_nvfp4(d, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 4 * k,
-                                  (ks > ks0 || k > 0) ? 1u : 0u);
-                    }
-                    mma_commit(bar);
+        const uint32_t n16 = (rows + 15) & ~15;
+        // E2M1 x E2M1, E4M3 scales, N = n16, M = 128
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((n16 >> 3) << 17) | ((uint32_t)(kM >> 7) << 27);
+        // One lane runs the whole row: its own instructions bound a short stage, and a choice
+        // of lane and an answer for the warp at every stage would add a third to them.
+        if (elect_one()) {
+            bool ready = false;
+            int st = 0;
+            uint32_t ph = 0, set = 0;
+            for (int ks = ks0; ks < ks1; ++ks) {
+                if (!ready && !lane_wait(smem_u32(&C.full[st]), ph, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                if (ok) mma_commit(smem_u32(&C.tfull[acc]));
+                fence_after();
+                const int nk = p.steps - 4 * ks < 4 ? p.steps - 4 * ks : 4;
+                const uint32_t at = st * (S::kStageBytes >> 4);  // addresses in descriptors count 16 bytes
+                const uint32_t ca = S::kScaleCol + set * S::kSetCols, cb = ca + 16, bar = smem_u32(&C.empty[st]);
+                if (++st == S::kStages) { st = 0; ph ^= 1; }
+                set ^= 1;
+                // a first look at the next stage, answered while this one's products are issued
+                ready = mbar_test(smem_u32(&C.full[st]), ph);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= nk) break;
+                    tmem_cp_scales(cb + 4 * k, desc_sb + (at + k * (kTileBytes >> 4)));
+                    tmem_cp_scales(ca + 4 * k, desc_sa + (at + k * (kTileBytes >> 4)));
+                    mma_nvfp4(0, desc_a + (at + 2 * k), desc_b + (at + 2 * k), idesc, ca + 4 * k, cb + 4 * k,
+                              (ks > ks0 || k > 0) ? 1u : 0u);
+                }
+                mma_commit(bar);
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            stage += ks1 - ks0;
-            phase ^= (stage / S::kStages) & 1;
-            stage %= S::kStages;
-            set ^= (ks1 - ks0) & 1;
-            if (++acc == 2) { acc = 0; aphase ^= 1; }
+            if (ok) mma_commit(smem_u32(&C.tfull));
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) {  // the products in flight end before the CTA does
             give_up(abort_flag);
             if (elect_one()) mma_commit(smem_u32(&C.done));
@@ -507,105 +469,76 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int none = 0;
             warp_wait(smem_u32(&C.done), 0, &none);
         }
-    } else if (!kSplit) {
-        if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int q = warp & 3;  // the TMEM lanes that this warp can read
-        uint8_t* turn = turn_p + ((warp - 2) >> 1) * kTurnBytes;
-        uint32_t half = 0;
-        int acc = 0;
-        uint32_t aphase = 0;
-        bool ok = true;
-        for (int64_t u = first; ok && walk.find(p, u, t); u += step) {
-            const float gw = __ldg(p.wg + t.g);
-            float gx[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                gx[j] = 32 * j + lane < t.rows ? gw * __ldg(p.xg + t.row0 + 32 * j + lane) : 0.0f;
-            ok = warp_wait(smem_u32(&C.tfull[acc]), aphase, abort_flag);
-            if (!ok) break;
-            fence_after();
-            Part<Tout> part;
-            part.take(tmem + ((uint32_t)(q * 32) << 16) + acc * kT, t.rows);
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&C.tempty[acc]));
-            if (++acc == 2) { acc = 0; aphase ^= 1; }
-            part.template put<0>(gx, t.rows, static_cast<Tout*>(p.Y) + t.row0 * p.ld_y, p.ld_y,
-                                     (int64_t)t.mt * kM + q * 32, p.c_out, turn, half, nullptr, 0);
-        }
-        if (!ok) give_up(abort_flag);
     } else {
         if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         if constexpr (kFused) write_tokens<Tin>(p, C, ring, ks0, ks1, abort_flag);
-        if (walk.find(p, first, t) && !warp_wait(smem_u32(&C.tfull[0]), 0, abort_flag)) give_up(abort_flag);
+        if (!warp_wait(smem_u32(&C.tfull), 0, abort_flag)) give_up(abort_flag);
     }
-    if constexpr (kSplit) {
-        // One tile: the ring is idle once all its products are done. Its first 64 KB take
-        // this CTA's sums, [token][channel], the next 64 KB those of the other parts for this
-        // CTA's tokens, [part][token][channel], sent by bulk copies.
-        const int per = (t.rows + parts - 1) / parts, q = warp & 3;
-        float* mine = reinterpret_cast<float*>(base_p);
-        float* theirs = mine + kT * kM;
-        auto tokens_of = [&](int r) {  // how many of its tokens the tile has
-            const int n = t.rows - r * per;
-            return n < 0 ? 0 : (n < per ? n : per);
-        };
-        const int64_t row0 = t.row0 + rank * per;
-        float gx[2] = {0.0f, 0.0f};  // of this CTA's tokens, one per lane (two parts: 64 tokens)
-        if (warp >= 2) {
-            const float gw = __ldg(p.wg + t.g);
+    // The ring is idle once all its products are done. Its first 64 KB take
+    // this CTA's sums, [token][channel], the next 64 KB those of the other parts for this
+    // CTA's tokens, [part][token][channel], sent by bulk copies.
+    const int per = (rows + parts - 1) / parts, q = warp & 3;
+    float* mine = reinterpret_cast<float*>(base_p);
+    float* theirs = mine + kT * kM;
+    auto tokens_of = [&](int r) {  // how many of its tokens the tile has
+        const int n = rows - r * per;
+        return n < 0 ? 0 : (n < per ? n : per);
+    };
+    const int64_t row0 = rank * per;
+    float gx[2] = {0.0f, 0.0f};  // of this CTA's tokens, one per lane (two parts: 64 tokens)
+    if (warp >= 2) {
+        const float gw = __ldg(p.wg);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (32 * j + lane < tokens_of(rank)) {
-                    if constexpr (kFused) gx[j] = gw * C.gscale[rank * per + 32 * j + lane];
-                    else gx[j] = gw * __ldg(p.xg + row0 + 32 * j + lane);
-                }
-            fence_after();
-            for (int c = 0; c < t.rows; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, r);
-                tmem_wait32(r);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mine[(c + i) * kM + q * 32 + lane] = __uint_as_float(r[i]);
+        for (int j = 0; j < 2; ++j)
+            if (32 * j + lane < tokens_of(rank)) {
+                if constexpr (kFused) gx[j] = gw * C.gscale[rank * per + 32 * j + lane];
+                else gx[j] = gw * __ldg(p.xg + row0 + 32 * j + lane);
             }
-            fence_proxy_async();
+        fence_after();
+        for (int c = 0; c < rows; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, r);
+            tmem_wait32(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mine[(c + i) * kM + q * 32 + lane] = __uint_as_float(r[i]);
         }
-        __syncthreads();
-        cluster_meet();  // the rings of all parts are idle
-        if (warp >= 2) {
-            const uint32_t bar = smem_u32(&C.sums), got = (parts - 1) * tokens_of(rank) * kM * 4;
-            if (warp == 2 && elect_one()) {
-                if (got) mbar_expect_tx(bar, got);
-                for (int r = 0; r < parts; ++r)
-                    if (r != rank && tokens_of(r) > 0)
-                        bulk_copy_cluster(cluster_addr(smem_u32(theirs + rank * per * kM), r), smem_u32(mine + r * per * kM),
-                                          tokens_of(r) * kM * 4, cluster_addr(bar, r));
-            }
-            __syncwarp();
-            if (got && !warp_wait(bar, 0, abort_flag)) give_up(abort_flag);
-            if (tokens_of(rank) > 0) {
-                const int64_t ch = (int64_t)t.mt * kM + q * 32 + lane;
-                Tout* y = static_cast<Tout*>(p.Y) + row0 * p.ld_y + ch;
-                const int n = tokens_of(rank);
-                for (int i0 = 0; i0 < n; i0 += 8) {  // the additions of eight tokens overlap
-                    float v[8] = {};
-                    for (int s = 0; s < parts; ++s) {
-                        const float* part = s == rank ? mine + rank * per * kM : theirs + s * per * kM;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i0 + i < n) v[i] += part[(i0 + i) * kM + q * 32 + lane];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float g = __shfl_sync(0xFFFFFFFFu, i0 < 32 ? gx[0] : gx[1], (i0 + i) & 31);
-                        if (i0 + i < n && ch < p.c_out) store_out(y + (int64_t)(i0 + i) * p.ld_y, v[i] * g);
-                    }
-                }
-            }
+        fence_proxy_async();
+    }
+    __syncthreads();
+    cluster_meet();  // the rings of all parts are idle
+    if (warp >= 2) {
+        const uint32_t bar = smem_u32(&C.sums), got = (parts - 1) * tokens_of(rank) * kM * 4;
+        if (warp == 2 && elect_one()) {
+            if (got) mbar_expect_tx(bar, got);
+            for (int r = 0; r < parts; ++r)
+                if (r != rank && tokens_of(r) > 0)
+                    bulk_copy_cluster(cluster_addr(smem_u32(theirs + rank * per * kM), r), smem_u32(mine + r * per * kM),
+                                      tokens_of(r) * kM * 4, cluster_addr(bar, r));
         }
         __syncwarp();
-        cluster_meet();  // nothing is in flight from or to a CTA that ends
+        if (got && !warp_wait(bar, 0, abort_flag)) give_up(abort_flag);
+        if (tokens_of(rank) > 0) {
+            const int64_t ch = (int64_t)mt * kM + q * 32 + lane;
+            Tout* y = static_cast<Tout*>(p.Y) + row0 * p.ld_y + ch;
+            const int n = tokens_of(rank);
+            for (int i0 = 0; i0 < n; i0 += 8) {  // the additions of eight tokens overlap
+                float v[8] = {};
+                for (int s = 0; s < parts; ++s) {
+                    const float* part = s == rank ? mine + rank * per * kM : theirs + s * per * kM;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i0 + i < n) v[i] += part[(i0 + i) * kM + q * 32 + lane];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float g = __shfl_sync(0xFFFFFFFFu, i0 < 32 ? gx[0] : gx[1], (i0 + i) & 31);
+                    if (i0 + i < n && ch < p.c_out) store_out(y + (int64_t)(i0 + i) * p.ld_y, v[i] * g);
+                }
+            }
+        }
     }
+    __syncwarp();
+    cluster_meet();  // nothing is in flight from or to a CTA that ends
     fence_before();
     __syncthreads();
     fence_after();
@@ -623,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
 constexpr int kPairWarps = 8;      // of the epilogue
 constexpr int kPairThreads = 64 + 32 * kPairWarps;  // producer, MMA, epilogue
-constexpr int kPairRows = 192;     // rows per group from which groups are given to pairs
+constexpr int kPairRows = 160;     // rows per group from which tiles of 256 tokens are taken
 
 template <int T>  // tokens of a tile: 256 or 128
 struct Pair {
@@ -890,29 +823,29 @@ bool make_out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, co
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kSplit, typename Tout, typename Tin = void>
-lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
-                         const ProdArgs& p, int parts, int sms, cudaStream_t st) {
+template <typename Tout, typename Tin = void>
+lh_status launch_split(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
+                       ProdArgs p, int parts, cudaStream_t st) {
     using S = Shape;
-    const int64_t xs_tiles = (p.n_rows / kTileRows + p.G) * p.steps, ws_tiles = p.G * p.mtiles128 * p.steps;
+    const int64_t xs_tiles = (p.n_rows / kTileRows + 1) * p.steps, ws_tiles = (int64_t)p.mtiles * p.steps;
     if (xs_tiles > INT_MAX - 512 || ws_tiles > INT_MAX - 512) return fail(LH_ERR_UNSUPPORTED, "too many scale tiles");
+    p.box = 16;  // the power of 2 that takes all tokens (a copy costs its rows, used or not, about 1.3 ns each)
+    while (p.box < p.n_rows) p.box *= 2;
     CUtensorMap wmap, xmap, wsmap, xsmap;
-    bool ok = make_map(encode, &wmap, W, p.G * p.c_out, c_in / 2, kM) && make_scale_map(encode, &wsmap, p.ws, ws_tiles);
+    bool ok = make_map(encode, &wmap, W, p.c_out, c_in / 2, kM) && make_scale_map(encode, &wsmap, p.ws, ws_tiles);
     if constexpr (std::is_void_v<Tin>)
         ok = ok && make_map(encode, &xmap, X, p.n_rows, c_in / 2, p.box) && make_scale_map(encode, &xsmap, p.xs, xs_tiles);
     else
         xmap = wmap, xsmap = wsmap;  // not used
     if (!ok) return fail(LH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    const int64_t tiles = (p.offsets ? p.n_rows / kT + p.G : (p.n_rows + kT - 1) / kT) * p.mtiles;  // at most
-    if (tiles > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "too many output tiles");
-    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 2 * kTurnBytes + 1024 + sizeof(Control);
+    constexpr size_t smem = (size_t)S::kStages * S::kStageBytes + 1024 + sizeof(Control);
     static_assert(smem <= 227 * 1024, "shared memory");
-    auto kernel = product_kernel<kSplit, Tout, Tin>;
+    auto kernel = product_split_kernel<Tout, Tin>;
     static std::atomic<uint64_t> done{0};
     lh_status s = allow_shared((const void*)kernel, smem, done);
     if (s != LH_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(kSplit ? tiles * parts : (tiles < sms ? tiles : sms)));
+    cfg.gridDim = dim3((unsigned)(p.mtiles * parts));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -923,8 +856,8 @@ lh_status launch_product(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t
     attr[1].val.clusterDim.x = (unsigned)parts;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_kernel launch");
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, wsmap, xsmap, p), "product_split_kernel launch");
 }
 
 int64_t pair_tiles(const ProdArgs& p, int T) {  // at most
@@ -984,26 +917,27 @@ int split_parts(const ProdArgs& p, int sms) {
     return 1;
 }
 
-// Which kernel. One matrix: CTA pairs above 128 tokens (160 x 4096 -> 12288: 13.1 us
-// against 16.1 us in two tiles of single CTAs; 128: 11.2 us single, 13.0 us in pairs), else
-// single CTAs, with c_in split over clusters while the tiles leave half of the SMs idle.
-// Groups, whose sizes the host does not know: pairs from 192 rows a group on (64 experts
-// 2048 -> 1536: 256 rows a group 54 us in pairs and 58 us in single CTAs, 128 rows a group
-// 42 and 39 us).
+// Which kernel. One matrix with tiles for at most half of the SMs: c_in split over clusters
+// while that takes stages away from a row for at most four tokens each, since more tokens make
+// the sums' way longer (4096 -> 4096, 12 of 16 stages: 32 tokens 5.9 us split and 6.8 us in
+// pairs, 64 tokens 7.5 and 7.3 us; 17408 -> 5120, 45 of 68: 128 tokens 17.3 and 19.8 us). Else
+// CTA pairs, with tiles of 256 tokens or, where these need more than 7/10 of the rounds of
+// 128-token tiles or groups are small, of 128: 300 x 4096 -> 4096 8.1 us against 9.7 us. Of
+// groups, whose sizes the host does not know, from 160 rows on average (64 experts 2048 -> 1536:
+// 128 rows each 29.2 us in tiles of 128 and 30.0 us of 256, 192 rows 38.0 and 32.4 us).
 template <typename Tout>
 lh_status dispatch(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X, const uint8_t* W, int64_t c_in,
                    const ProdArgs& p, int sms, cudaStream_t st) {
-    if (p.offsets ? p.n_rows >= kPairRows * p.G : p.n_rows > kT) {
-        const int64_t pairs = sms / 2;
-        auto rounds = [&](int T) { return (pair_tiles(p, T) + pairs - 1) / pairs; };
-        if (!p.offsets && 7 * rounds(128) < 10 * rounds(256)) return launch_pair<128, Tout>(encode, X, W, c_in, p, sms, st);
-        return launch_pair<256, Tout>(encode, X, W, c_in, p, sms, st);
+    if (!p.offsets && p.n_rows <= kT) {
+        const int parts = split_parts(p, sms), saved = p.stages_k - (p.stages_k + parts - 1) / parts;
+        if (parts > 1 && p.n_rows <= (saved < 4 ? 16 : 4 * saved))
+            return launch_split<Tout>(encode, X, W, c_in, p, parts, st);
     }
-    if (!p.offsets) {
-        const int parts = split_parts(p, sms);
-        if (parts > 1) return launch_product<true, Tout>(encode, X, W, c_in, p, parts, sms, st);
-    }
-    return launch_product<false, Tout>(encode, X, W, c_in, p, 1, sms, st);
+    const int64_t pairs = sms / 2;
+    auto rounds = [&](int T) { return (pair_tiles(p, T) + pairs - 1) / pairs; };
+    if (p.offsets ? p.n_rows < kPairRows * p.G : 7 * rounds(128) < 10 * rounds(256))
+        return launch_pair<128, Tout>(encode, X, W, c_in, p, sms, st);
+    return launch_pair<256, Tout>(encode, X, W, c_in, p, sms, st);
 }
 
 lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale, const int64_t* offsets,
@@ -1038,10 +972,6 @@ ProdArgs product_args(const uint8_t* X_scales, const float* X_gscale, const uint
     p.mtiles = p.mtiles128 = (int)((c_out + kM - 1) / kM);
     p.stages_k = (int)((c_in + kStageK - 1) / kStageK);
     p.steps = (int)scale_steps(c_in);
-    // the power of 2 that takes a group of average size in one copy (a copy costs its rows,
-    // used or not, about 1.3 ns each)
-    p.box = 16;
-    while (p.box < kT && p.box * n_groups < n_rows) p.box *= 2;
     p.xs = X_scales; p.ws = W_scales; p.xg = X_gscale; p.wg = W_gscale; p.Y = Y; p.early = early;
     return p;
 }
@@ -1089,11 +1019,11 @@ lh_status fused(ProdArgs p, const void* X, lh_dtype x_dtype, int64_t c_in, int64
     const int parts = split_parts(p, sms);
     if (x_dtype == LH_BF16)
         return out_dtype == LH_BF16
-                   ? launch_product<true, __nv_bfloat16, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, sms, st)
-                   : launch_product<true, float, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, sms, st);
+                   ? launch_split<__nv_bfloat16, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, st)
+                   : launch_split<float, uint16_t>(encode, nullptr, W_packed, c_in, p, parts, st);
     return out_dtype == LH_BF16
-               ? launch_product<true, __nv_bfloat16, float>(encode, nullptr, W_packed, c_in, p, parts, sms, st)
-               : launch_product<true, float, float>(encode, nullptr, W_packed, c_in, p, parts, sms, st);
+               ? launch_split<__nv_bfloat16, float>(encode, nullptr, W_packed, c_in, p, parts, st)
+               : launch_split<float, float>(encode, nullptr, W_packed, c_in, p, parts, st);
 }
 
 }  // namespace
