@@ -547,12 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_split_kernel(const __grid
 
 // ---------------------------------------------------------------- CTA pairs
 //
-// Tiles of 256 channels x 256 tokens, one per pair of CTAs (cta_group::2): each CTA
-// loads its own 128 channels and half of the tokens, so a stage brings 38 KB for
-// 128 x 256 x 256 products where a tile of 128 x 128 brings 36 KB for half of them. The
-// scales of all 256 tokens go to both CTAs. The accumulator takes 256 TMEM columns and
-// the scales 96, which leaves no room for a second one: eight epilogue warps take a
-// whole accumulator into registers and free it before they scale and store.
+// Tiles of 256 channels x T tokens, one per pair of CTAs (cta_group::2): each CTA loads its
+// own 128 channels and half of the tokens, so for T = 256 a stage brings 38 KB for 128 x 256 x
+// 256 products where a tile of one CTA, 128 x 128, brings 36 KB for half of them. The scales
+// of all tokens go to both CTAs. The accumulator takes 256 TMEM columns and the scales 96,
+// which leaves no room for a second one: eight epilogue warps take a whole accumulator into
+// registers and free it, some 570 clocks in all, before they scale and store beside the next
+// tile's products. 8192 x 4096 -> 12288 takes 155 us (5.3 PFLOP/s, 81 % of four times the
+// measured bf16 rate): a stage takes 520 to 640 clocks of which the products need 512.
+// T = 128 leaves room for seven stages instead of five and suits few or small tiles; a
+// stage takes 480 clocks there, the issuing lane's own instructions.
 
 constexpr int kPairWarps = 8;      // of the epilogue
 constexpr int kPairThreads = 64 + 32 * kPairWarps;  // producer, MMA, epilogue
@@ -908,7 +912,7 @@ lh_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t* X
 }
 
 // Parts of c_in for the tiles of one matrix and at most 128 tokens: as many as SMs allow, in
-// cluster sizes that pack the GPCs (1 x 17408 -> 5120, 40 tiles: 21.2 us in two parts, 18.4 us
+// cluster sizes that pack the GPCs (1 x 17408 -> 5120, 40 tiles: 12.6 us in two parts, 10.0 us
 // in three).
 int split_parts(const ProdArgs& p, int sms) {
     const int most = p.mtiles > 0 ? sms / p.mtiles : 1;
@@ -1002,9 +1006,9 @@ lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* 
 }
 
 // Whether the product takes the tokens themselves: one matrix in few tiles, and so little of
-// them that every CTA can look at it all. From the tokens on, 1 x 4096 -> 4096 takes 7.3 us so
-// and 7.4 us in two launches, with 2.3 us less of the host's time; 2 tokens take 7.9 and
-// 7.5 us, 1 x 17408 -> 5120 24.8 and 21.2 us.
+// them that every CTA can look at it all. From the tokens on, 1 x 4096 -> 4096 takes 6.5 us so
+// and 6.4 us in two launches, 1 x 2048 -> 1536 5.3 and 5.6 us, both with 2.3 us less of the
+// host's time; for 2 x 4096 values or 1 x 17408 the device takes longer so.
 bool can_fuse(const ProdArgs& p, int64_t c_in, const int32_t* rows, int sms) {
     return !rows && !p.offsets && p.n_rows <= kFewTokens && p.n_rows * c_in <= 4096 && split_parts(p, sms) > 1;
 }
