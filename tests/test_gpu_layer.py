@@ -433,6 +433,35 @@ def test_grouped_product_of_whole_numbers_is_exact(cuda_ok, counts, before, afte
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,m,c", [
+    ([1500], 5000, 2080), ([2000], 4999, 96), ([1100], 5121, 1280),   # several rounds of 256-token tiles
+    ([100] * 40, 1100, 1312), ([1, 120, 0, 64, 33] * 12, 1000, 1824),  # and of 128-token tiles, one and two a group
+    ([400] * 12, 1300, 1600), ([290, 0, 161, 32, 384] * 8, 520, 2336),
+])
+def test_many_tiles_for_every_pair(cuda_ok, counts, m, c, t):
+    # the ring, the scales' places and the halves of the way to Y go on from tile to tile
+    rng = np.random.default_rng(len(counts) + m)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    n, G = int(off[-1]), len(counts)
+    xp, xc = whole_operand(rng, (n, c))
+    wp, wc = whole_operand(rng, (G, m, c))
+    xg = np.exp2(rng.integers(-3, 4, n)).astype(np.float32)
+    wg = np.exp2(rng.integers(-3, 4, G)).astype(np.float32)
+    y = torch.full((n + 1, pitch(m, t)), 11.0, dtype=DT[t], device="cuda")
+    given = off if G > 1 else None
+    matmul(torch.from_numpy(xp).cuda(), token_tiles(xc, given), torch.from_numpy(xg).cuda(), torch.from_numpy(wp).cuda(),
+           tiles_of(wc), torch.from_numpy(wg).cuda(), None if G == 1 else torch.from_numpy(off).cuda(), y, m, c)
+    for g in range(G):
+        a, b = off[g], off[g + 1]
+        if b > a:
+            x = torch.from_numpy(ref.decode(xp[a:b], xc[a:b])).double()
+            w = torch.from_numpy(ref.decode(wp[g], wc[g])).double()
+            want = (x @ w.T) * torch.from_numpy(xg[a:b]).double()[:, None] * float(wg[g])
+            assert torch.equal(y[a:b, :m].cpu(), want.float().to(DT[t]))
+    assert (y[n:] == 11.0).all() and (y[:, m:] == 11.0).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
 @pytest.mark.parametrize("n,m,c", [(1, 256, 4096), (60, 384, 1024), (300, 130, 17408)])
 def test_product_of_quantised_tokens(cuda_ok, n, m, c, t):
     # every scale code and value that quantisation makes, against FP64 with the bound of FP32 sums
