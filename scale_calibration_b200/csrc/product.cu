@@ -72,7 +72,7 @@ struct Shape {
     static_assert(kStages * kStageBytes >= 2 * kT * kM * 4, "split: the partial sums reuse the ring");
 };
 
-constexpr int kFewTokens = 8;  // most tokens that the product quantises itself
+constexpr int kFewTokens = 4;  // most tokens that the product quantises itself
 
 struct Control {
     uint32_t amax[4][kFewTokens];  // of the tokens, by warp
@@ -1007,10 +1007,11 @@ lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* 
 
 // Whether the product takes the tokens themselves: one matrix in few tiles, and so little of
 // them that every CTA can look at it all. From the tokens on, 1 x 4096 -> 4096 takes 6.5 us so
-// and 6.4 us in two launches, 1 x 2048 -> 1536 5.3 and 5.6 us, both with 2.3 us less of the
-// host's time; for 2 x 4096 values or 1 x 17408 the device takes longer so.
+// and 6.4 us in two launches, 1 x 8192 -> 4096 7.8 and 8.0 us, 4 x 2048 -> 1536 5.9 and 6.0 us,
+// with a launch less of the host's time each; 8 x 1024 -> 1024 takes 6.7 and 5.6 us,
+// 4 x 4096 -> 4096 8.2 and 6.5 us.
 bool can_fuse(const ProdArgs& p, int64_t c_in, const int32_t* rows, int sms) {
-    return !rows && !p.offsets && p.n_rows <= kFewTokens && p.n_rows * c_in <= 4096 && split_parts(p, sms) > 1;
+    return !rows && !p.offsets && p.n_rows <= kFewTokens && p.n_rows * c_in <= 8192 && split_parts(p, sms) > 1;
 }
 
 // The product of few tokens, from the tokens on. Arguments as lh_nvfp4_linear has checked them.
