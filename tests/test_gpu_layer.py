@@ -619,6 +619,14 @@ def test_linear_of_few_tokens_equals_its_two_calls(cuda_ok, n, m, c, given, t):
     assert lh.lh_nvfp4_status() == 0
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("given", [None, 3.0])
+@pytest.mark.parametrize("n,m,c", [(1, 4096, 8192), (1, 130, 8224), (2, 200, 4096), (3, 257, 2720), (4, 1536, 2048),
+                                   (4, 9000, 480), (5, 300, 1024)])
+def test_the_most_tokens_of_one_launch(cuda_ok, n, m, c, given, t):
+    test_linear_of_few_tokens_equals_its_two_calls(cuda_ok, n, m, c, given, t)
+
+
 def test_linear_of_tokens_that_are_not_finite(cuda_ok):
     rng = np.random.default_rng(2)
     w, wv, wg = bank(rng, 1, 200, 128)
