@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(256, sizeof(Tin) == 2 && !kOut ? 4 : 3)
         }
         return m;
     };
-    for (int row = blockIdx.x * kRows + part; row < p.n_rows; row += gridDim.x * kRows) {
+    // unsigned: the step past the last of up to 2^31 - 513 rows would overflow an int
+    for (uint32_t row = blockIdx.x * kRows + part; row < (uint32_t)p.n_rows; row += gridDim.x * kRows) {
         int g, lo;
-        if (!find_group(p, row, g, lo)) continue;
+        if (!find_group(p, (int)row, g, lo)) continue;
         int64_t src = row;
         if (p.rows) {
             const int f = __ldg(p.rows + row);

@@ -1,0 +1,56 @@
+"""The operators that run a calibrated layer at the ends of what they accept, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+from tests import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _lh():
+    import scale_calibration_b200 as lh
+    return lh
+
+
+@pytest.fixture
+def big(cuda_ok):
+    """Room for tens of GB, given back afterwards."""
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+PIECE = 1 << 27  # rows looked at together
+
+
+def test_the_most_rows_of_tokens(big):
+    # 2^31 - 513 rows of one block each: a counter of rows that steps past the last one must not come round again
+    lh = _lh()
+    n, c, n_src = (1 << 31) - 513, 16, 37
+    v = np.random.default_rng(0).standard_normal((n_src, c)).astype(np.float32)
+    x = torch.from_numpy(v).cuda()
+    rows = torch.empty(n, dtype=torch.int32, device="cuda")
+    for a in range(0, n, PIECE):
+        b = min(a + PIECE, n)
+        rows[a:b] = (torch.arange(a, b, device="cuda") % n_src).to(torch.int32)
+    packed = torch.zeros(n, c // 2, dtype=torch.uint8, device="cuda")
+    tiles = torch.zeros(lh.lh_nvfp4_token_scale_bytes(n, c, 1), dtype=torch.uint8, device="cuda")
+    g = torch.zeros(n, device="cuda")
+    lh.lh_quantize_tokens(x, x, n_src, c, c, rows, 1, n, None, 1, None, packed, tiles, g)
+    rp, rc, rg, _ = ref.quantize_tokens(v)
+    rp, rg, rc = (torch.from_numpy(a.copy()).cuda() for a in (rp, rg, rc))
+    rp = rp.view(torch.int64).view(-1)
+    packed = packed.view(torch.int64).view(-1)
+    for a in range(0, n, PIECE):
+        b = min(a + PIECE, n)
+        i = rows[a:b].long()
+        assert torch.equal(g[a:b], rg[i])
+        assert torch.equal(packed[a:b], rp[i])
+    # row r's code: byte 0 of (r % 32, r % 128 / 32) of tile r / 128
+    words = tiles.view(torch.int32).view(-1, 32, 4)
+    for t0 in range(0, words.shape[0], PIECE // 128):
+        w = words[t0:t0 + PIECE // 128].permute(0, 2, 1).reshape(-1)
+        a, b = 128 * t0, min(128 * t0 + w.numel(), n)
+        assert torch.equal(w[:b - a], rc.view(-1)[rows[a:b].long()].to(torch.int32))
