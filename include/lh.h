@@ -335,7 +335,8 @@ LH_API lh_status lh_search_amax(const void* W, lh_dtype w_dtype, int64_t n_mats,
  * ids: device int32 [n_tok][k]. offsets: device int64 [n_experts + 1]. order, pos:
  *   device int32 [n_tok * k]. All of them are written in full.
  * One launch; n_tok == 0 only writes zero offsets.
- * LH_ERR_UNSUPPORTED: n_experts > 1024, or n_tok * k >= 2^31.
+ * LH_ERR_UNSUPPORTED: n_experts > 1024, or n_tok * k >= 2^31 - 512 (the same limit
+ * holds for the two combination calls below).
  * ---------------------------------------------------------------------- */
 LH_API lh_status lh_route_tokens(const int32_t* ids, int64_t n_tok, int64_t k, int64_t n_experts, int64_t* offsets,
                                  int32_t* order, int32_t* pos, void* stream);

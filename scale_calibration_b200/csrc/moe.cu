@@ -476,10 +476,14 @@ bool wide_rows(const void* p, lh_dtype t, int64_t ld) {
     return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (ld * elem_bytes(t)) % 32 == 0;
 }
 
+constexpr int64_t kMaxFlat = INT_MAX - 512;
+static_assert(32 * kHeldIds + 32 <= 512 && kSlots <= 512, "steps past the last flat index");
+
 lh_status check_slots(int64_t n_tok, int64_t k) {
     if (n_tok < 0 || k < 1) return fail(LH_ERR_INVALID_ARG, "n_tok must be >= 0 and k >= 1");
-    if (k > INT_MAX || (n_tok > 0 && n_tok > INT_MAX / k))
-        return fail(LH_ERR_UNSUPPORTED, "n_tok * k must be below 2^31");
+    // the kernels' 32-bit counters of flat indices and slots step past the last one
+    if (k > kMaxFlat || (n_tok > 0 && n_tok > kMaxFlat / k))
+        return fail(LH_ERR_UNSUPPORTED, "n_tok * k must be below 2^31 - 512");
     return LH_OK;
 }
 

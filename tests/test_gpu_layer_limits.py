@@ -54,3 +54,24 @@ def test_the_most_rows_of_tokens(big):
         w = words[t0:t0 + PIECE // 128].permute(0, 2, 1).reshape(-1)
         a, b = 128 * t0, min(128 * t0 + w.numel(), n)
         assert torch.equal(w[:b - a], rc.view(-1)[rows[a:b].long()].to(torch.int32))
+
+
+def test_the_most_ids(big):
+    # 2^31 - 513 ids, every third of them without an expert
+    lh = _lh()
+    n, e = (1 << 31) - 513, 2
+    ids = torch.empty(n, dtype=torch.int32, device="cuda")
+    for a in range(0, n, PIECE):
+        b = min(a + PIECE, n)
+        ids[a:b] = (torch.arange(a, b, device="cuda") % 3).to(torch.int32)
+    off = torch.zeros(e + 1, dtype=torch.int64, device="cuda")
+    order, pos = (torch.full((n,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    lh.lh_route_tokens(ids, n, 1, e, off, order, pos)
+    n0, n1 = -(-n // 3), -(-(n - 1) // 3)
+    assert off.tolist() == [0, n0, n0 + n1]
+    for a in range(0, n, PIECE):
+        p = torch.arange(a, min(a + PIECE, n), device="cuda")
+        want = torch.where(p < n0, 3 * p, torch.where(p < n0 + n1, 3 * (p - n0) + 1, -1))
+        assert torch.equal(order[a:a + len(p)], want.to(torch.int32))
+        want = torch.where(p % 3 == 0, p // 3, torch.where(p % 3 == 1, p // 3 + n0, -1))
+        assert torch.equal(pos[a:a + len(p)], want.to(torch.int32))

@@ -1,0 +1,23 @@
+"""What the operators that run a calibrated layer accept and refuse at the ends of their ranges (no GPU)."""
+import pytest
+
+FAKE = 0x10000000  # never dereferenced: validation fails first, or there is nothing to do
+MOST = (1 << 31) - 513  # flat slots, rows
+
+
+def _lh():
+    import scale_calibration_b200 as lh
+    return lh
+
+
+@pytest.mark.parametrize("n,k", [(MOST + 1, 1), (1, MOST + 1), ((1 << 31) - 1, 1), (1, (1 << 31) - 1), (1 << 28, 8),
+                                 (715827712, 3)])
+def test_flat_indices_that_a_32_bit_counter_would_step_past_are_refused(n, k):
+    lh = _lh()
+    assert lh.lh_route_tokens(FAKE, n, k, 4, FAKE + 4096, FAKE + 8192, FAKE + 16384, 0, False) == 2
+    assert lh.lh_combine_tokens(FAKE, lh.LH_F32, 8, 8, 8, FAKE, None, n, k, FAKE + 65536, 8, 0, False) == 2
+    assert lh.lh_combine_tokens_grad(FAKE, lh.LH_F32, n, k, 8, 8, FAKE + 65536, 8, 8, FAKE, None, FAKE + 131072, 8, FAKE,
+                                     0, False) == 2
+    # one slot less is no matter of sizes: other checks answer
+    if n == MOST + 1:
+        assert lh.lh_route_tokens(0, n - 1, k, 4, FAKE + 4096, FAKE + 8192, FAKE + 16384, 0, False) == 1
