@@ -442,7 +442,8 @@ LH_API lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t n_s
  *   f32 [n_groups], as lh_quantize_nvfp4 writes them; W_scales: lh_nvfp4_tile_scales.
  * Y: device bf16 (round to nearest even) or f32 [n_rows][ld_y]; rows in no group and
  *   columns from c_out to ld_y are left as they were.
- * c_in: a positive multiple of 32. n_rows, c_in and n_groups * c_out below 2^31 - 512.
+ * c_in: a positive multiple of 32, at most 2^28. n_rows and n_groups * c_out below
+ *   2^31 - 512.
  * Waits inside the kernel are bounded (1 s). One that gives up leaves Y incomplete and
  * is reported by lh_nvfp4_status, which synchronises `stream`, returns LH_ERR_TIMEOUT
  * if that happened on the current device since the last call, and clears it.

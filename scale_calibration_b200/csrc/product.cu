@@ -954,12 +954,14 @@ lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const 
     if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
     if (c_in % 32 != 0 || c_in == 0)
         return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a positive multiple of 32", (long long)c_in);
+    // the tokens' limit: 2^20 stages of some 0.3 us, so that the wait for a tile stays well within its 1 s
+    if (c_in > (1 << 28)) return fail(LH_ERR_UNSUPPORTED, "c_in must be at most 2^28");
     if (ld_y < c_out) return fail(LH_ERR_INVALID_ARG, "ld_y=%lld < c_out=%lld", (long long)ld_y, (long long)c_out);
     if (!aligned16(W_packed) || !aligned16(W_scales) || !aligned16(Y) || (ld_y * elem_bytes(out_dtype)) % 16 != 0)
         return fail(LH_ERR_ALIGNMENT, "W_packed, W_scales and Y must be 16-byte aligned, with 16-byte aligned rows of Y");
     // row and column coordinates of the TMA copies are 32-bit
-    if (n_rows > INT_MAX - 512 || c_in > INT_MAX - 512 || (c_out > 0 && n_groups > (INT_MAX - 512) / c_out))
-        return fail(LH_ERR_UNSUPPORTED, "rows, c_in and n_groups * c_out must be below 2^31 - 512");
+    if (n_rows > INT_MAX - 512 || (c_out > 0 && n_groups > (INT_MAX - 512) / c_out))
+        return fail(LH_ERR_UNSUPPORTED, "rows and n_groups * c_out must be below 2^31 - 512");
     return LH_OK;
 }
 

@@ -21,3 +21,14 @@ def test_flat_indices_that_a_32_bit_counter_would_step_past_are_refused(n, k):
     # one slot less is no matter of sizes: other checks answer
     if n == MOST + 1:
         assert lh.lh_route_tokens(0, n - 1, k, 4, FAKE + 4096, FAKE + 8192, FAKE + 16384, 0, False) == 1
+
+
+@pytest.mark.parametrize("c_in", [(1 << 28) + 32, (1 << 31) - 1024])
+def test_products_longer_than_any_quantised_token_are_refused(c_in):
+    # a tile of 2^31 columns takes more than two seconds, longer than the kernel's waits for it
+    lh = _lh()
+
+    def call(c, n=0):
+        return lh.lh_nvfp4_matmul(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, 1, n, 8, c, FAKE + 65536, lh.LH_F32, 8, 0, False)
+
+    assert call(c_in) == 2 and call(1 << 28) == 0
