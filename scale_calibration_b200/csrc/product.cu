@@ -413,6 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_split_kernel(const __grid
                 }
                 if (++st == S::kStages) { st = 0; ph ^= 1; }
             }
+            // the products' last arrivals on the ring come before the CTA ends
+            for (int i = n < S::kStages ? 0 : n - S::kStages; ok && i < n; ++i)
+                ok = lane_wait(smem_u32(&C.empty[i % S::kStages]), (i / S::kStages) & 1, abort_flag);
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         n = __reduce_max_sync(0xFFFFFFFFu, n);
@@ -671,9 +674,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             phase ^= (stage / S::kStages) & 1;
             stage %= S::kStages;
         }
+        const int last = issued < S::kStages ? (int)issued : S::kStages;
+        if (ok && elect_one()) {  // the products' last arrivals on this CTA's ring come before it ends
+            int st = stage;
+            uint32_t ph = phase;
+            for (int i = 0; ok && i < last; ++i) {
+                if (--st < 0) { st = S::kStages - 1; ph ^= 1; }
+                ok = lane_wait(smem_u32(&C.empty[st]), ph, abort_flag);
+            }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) {  // the loads in flight land before the CTAs end (both report to the first one's barriers)
             give_up(abort_flag);
-            const int n = rank == 0 ? (issued < S::kStages ? (int)issued : S::kStages) : 0;
+            const int n = rank == 0 ? last : 0;
             for (int i = 0; i < n; ++i) {
                 if (--stage < 0) { stage = S::kStages - 1; phase ^= 1; }
                 int none = 0;

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from tests import layer_ref as ref
+from tests import test_gpu_layer as layer
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,28 @@ def test_the_most_ids(big):
         assert torch.equal(order[a:a + len(p)], want.to(torch.int32))
         want = torch.where(p % 3 == 0, p // 3, torch.where(p % 3 == 1, p // 3 + n0, -1))
         assert torch.equal(pos[a:a + len(p)], want.to(torch.int32))
+
+
+@pytest.mark.parametrize("n,m,grouped", [(3, 200, False), (16, 130, False), (200, 300, False), (700, 520, False), (90, 300, True)])
+def test_rows_of_every_number_of_stages_one_after_another(cuda_ok, n, m, grouped):
+    # a kernel waits for the last arrivals on its ring, whatever is left over of it: split and paired products of one
+    # stage to three rings, launched back to back, all right and none of their waits run out
+    rng = np.random.default_rng(n)
+    calls = []
+    for stages in range(1, 22):
+        c = 256 * stages - 32 * int(rng.integers(8))
+        xp, xc = layer.whole_operand(rng, (n, c))
+        wp, wc = layer.whole_operand(rng, (1, m, c))
+        xg = np.exp2(rng.integers(-3, 4, n)).astype(np.float32)
+        off = np.array([0, n], np.int64) if grouped else None
+        a = (torch.from_numpy(xp).cuda(), layer.token_tiles(xc, off), torch.from_numpy(xg).cuda(), torch.from_numpy(wp).cuda(),
+             layer.tiles_of(wc), torch.tensor([0.5], device="cuda"), torch.from_numpy(off).cuda() if grouped else None)
+        x, w = (torch.from_numpy(v).double() for v in (ref.decode(xp, xc), ref.decode(wp[0], wc[0])))
+        want = ((x @ w.T) * torch.from_numpy(xg).double()[:, None] * 0.5).float()
+        calls.append((a, c, want, torch.empty(n, layer.pitch(m, "f32"), device="cuda")))
+    for _ in range(20):
+        for a, c, _, y in calls:
+            _lh().lh_nvfp4_matmul(*a, 1, n, m, c, y, y, y.stride(0))
+    for a, c, want, y in calls:
+        assert torch.equal(y[:, :m].cpu(), want), c
+    assert _lh().lh_nvfp4_status() == 0
