@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_split_kernel(const __grid
             if (ok) mma_commit(smem_u32(&C.tfull));
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) {  // the products in flight end before the CTA does
+        if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) {  // the products in flight end before the CTA does
             give_up(abort_flag);
             if (elect_one()) mma_commit(smem_u32(&C.done));
             __syncwarp();
@@ -692,6 +692,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 int none = 0;
                 warp_wait(smem_u32(&C.full[stage]), phase, &none);
             }
+            // the second CTA's may be of stages that the first never came to: no barrier here tells, so they get
+            // 1 ms, a thousand times what a load takes
+            if (rank != 0)
+                for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) {}
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 set ^= p.stages_k & 1;
                 aphase ^= 1;
             }
-            if (!ok) {  // the products in flight end before the CTAs do
+            if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) {  // the products in flight end before the CTAs do
                 give_up(abort_flag);
                 if (elect_one()) mma_commit_pair(smem_u32(&C.done));
                 __syncwarp();
