@@ -749,6 +749,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 set ^= p.stages_k & 1;
                 aphase ^= 1;
             }
+            // the second CTA's last arrivals come before this one ends
+            if (ok) ok = warp_wait(smem_u32(&C.tempty), aphase ^ 1, abort_flag);
             if (__any_sync(0xFFFFFFFFu, !ok || *abort_flag)) {  // the products in flight end before the CTAs do
                 give_up(abort_flag);
                 if (elect_one()) mma_commit_pair(smem_u32(&C.done));
