@@ -1095,7 +1095,8 @@ extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_
     clear_error();
     lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
     if (s != LH_OK) return s;
-    if (X == Y) return fail(LH_ERR_INVALID_ARG, "Y must not alias an input");
+    if (Y == X || Y == (const void*)W_packed || Y == (const void*)W_scales || Y == workspace)
+        return fail(LH_ERR_INVALID_ARG, "Y must not alias an input or the workspace");
     const size_t need = lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(LH_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,

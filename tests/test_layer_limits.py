@@ -32,3 +32,25 @@ def test_products_longer_than_any_quantised_token_are_refused(c_in):
         return lh.lh_nvfp4_matmul(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, 1, n, 8, c, FAKE + 65536, lh.LH_F32, 8, 0, False)
 
     assert call(c_in) == 2 and call(1 << 28) == 0
+
+
+def linear_args(**over):
+    lh = _lh()
+    a = dict(X=FAKE, x_dtype=lh.LH_F32, n_src=10, c_in=64, ld_x=64, rows=None, row_div=1, n_rows=0, offsets=None,
+             n_groups=1, global_amax=None, W_packed=FAKE + 262144, W_scales=FAKE + 524288, W_gscale=FAKE + 589824,
+             c_out=100, Y=FAKE + 65536, out_dtype=lh.LH_F32, ld_y=100, workspace=FAKE + 131072, workspace_bytes=4096,
+             stream=0, check=False)
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("n_rows", [0, 1, 10])
+def test_linear_refuses_an_output_over_its_weights_or_workspace(n_rows):
+    # whichever kernel the sizes choose: one row is quantised by the product, ten are not
+    lh = _lh()
+    assert lh.lh_nvfp4_linear(**linear_args()) == 0
+    for y in ("X", "W_packed", "W_scales", "workspace"):
+        a = linear_args(n_rows=n_rows)
+        a["Y"] = a[y]
+        assert lh.lh_nvfp4_linear(**a) == 1, y
+        assert "alias" in lh.lh_last_error_message()
