@@ -25,6 +25,9 @@
  *   - bf16 and f32 element pointers must be 16-byte aligned and leading
  *     dimensions must keep every row 16-byte aligned (LH_ERR_ALIGNMENT).
  *   - Outputs must not alias inputs.
+ *   - A call whose sizes leave nothing to do returns LH_OK; where an array has no
+ *     element for that reason its pointer may be NULL in the calls that run a
+ *     calibrated layer, and X's in the Hessian's.
  *   - Thread safety: calls are re-entrant; the only host state is a
  *     thread-local error message.
  */

@@ -19,6 +19,8 @@ lh_status cuda_status(cudaError_t e, const char* what);
 // Clears the thread-local message (start of every entry point).
 void clear_error();
 
+// The same array; empty ones (null) are not.
+inline bool same_array(const void* a, const void* b) { return a && a == b; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t elem_bytes(lh_dtype t) { return t == LH_BF16 ? 2 : 4; }
 inline bool valid_dtype(int t) { return t == LH_BF16 || t == LH_F32; }

@@ -721,7 +721,7 @@ unsigned long long next_generation() {
 lh_status validate_hessian_args(const void* X, lh_dtype x_dtype, int64_t n_tokens_total, int64_t c_in, int64_t ld_x,
                                 const int64_t* offsets, int64_t n_groups, const float* H) {
     if (x_dtype != LH_BF16) return fail(LH_ERR_UNSUPPORTED, "X must be LH_BF16");
-    if (!X || !H) return fail(LH_ERR_INVALID_ARG, "null X or H");
+    if ((!X && n_tokens_total != 0) || !H) return fail(LH_ERR_INVALID_ARG, "null X or H");
     if (n_tokens_total < 0 || c_in < 0 || n_groups < 1)
         return fail(LH_ERR_INVALID_ARG, "n_tokens_total, c_in must be >= 0 and n_groups >= 1");
     if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "offsets == NULL requires n_groups == 1");

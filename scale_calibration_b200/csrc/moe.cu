@@ -549,14 +549,15 @@ extern "C" lh_status lh_gather_tokens(const void* X, lh_dtype dtype, int64_t n_t
     using namespace lh;
     clear_error();
     if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
-    if (!X || !order || !Xs) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_tok < 0 || c < 0 || k < 1 || n_rows < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, k >= 1");
+    const bool nothing = n_tok == 0 || c == 0 || n_rows == 0;
+    if (!nothing && (!X || !order || !Xs)) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (k > INT_MAX) return fail(LH_ERR_UNSUPPORTED, "k must be below 2^31");
-    if (X == Xs) return fail(LH_ERR_INVALID_ARG, "Xs must not alias X");
+    if (same_array(X, Xs)) return fail(LH_ERR_INVALID_ARG, "Xs must not alias X");
     lh_status s = check_rows("X", X, dtype, c, ld_x);
     if (s == LH_OK) s = check_rows("Xs", Xs, dtype, c, ld_xs);
     if (s != LH_OK) return s;
-    if (n_tok == 0 || c == 0 || n_rows == 0) return LH_OK;
+    if (nothing) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     const bool wide = wide_rows(X, dtype, ld_x) && wide_rows(Xs, dtype, ld_xs);
@@ -580,13 +581,14 @@ extern "C" lh_status lh_combine_tokens(const void* Ys, lh_dtype dtype, int64_t n
     if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
     lh_status s = check_slots(n_tok, k);
     if (s != LH_OK) return s;
-    if (!Ys || !pos || !Y) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_rows < 0 || c < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0");
-    if (Y == Ys) return fail(LH_ERR_INVALID_ARG, "Y must not alias Ys");
+    const bool nothing = n_tok == 0 || c == 0;
+    if (!nothing && ((!Ys && n_rows > 0) || !pos || !Y)) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (same_array(Y, Ys)) return fail(LH_ERR_INVALID_ARG, "Y must not alias Ys");
     s = check_rows("Ys", Ys, dtype, c, ld_ys);
     if (s == LH_OK) s = check_rows("Y", Y, dtype, c, ld_y);
     if (s != LH_OK) return s;
-    if (n_tok == 0 || c == 0) return LH_OK;
+    if (nothing) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     const bool wide = wide_rows(Ys, dtype, ld_ys) && wide_rows(Y, dtype, ld_y);
@@ -611,16 +613,19 @@ extern "C" lh_status lh_combine_tokens_grad(const void* dY, lh_dtype dtype, int6
     if (!valid_dtype(dtype)) return fail(LH_ERR_UNSUPPORTED, "dtype %d is not LH_BF16 or LH_F32", (int)dtype);
     lh_status s = check_slots(n_tok, k);
     if (s != LH_OK) return s;
-    if (!dY || !pos) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
-    if (!dYs && !dweights) return fail(LH_ERR_INVALID_ARG, "one of dYs and dweights is needed");
-    if (dweights && !Ys) return fail(LH_ERR_INVALID_ARG, "dweights needs Ys");
     if (n_rows < 0 || c < 0) return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0");
-    if (dYs == dY || (dYs && dYs == Ys)) return fail(LH_ERR_INVALID_ARG, "dYs must not alias an input");
+    const bool no_rows = n_rows == 0 || c == 0;  // of Ys and dYs
+    if (n_tok > 0) {
+        if ((!dY && c > 0) || !pos) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+        if (!dYs && !dweights && !no_rows) return fail(LH_ERR_INVALID_ARG, "one of dYs and dweights is needed");
+        if (dweights && !Ys && !no_rows) return fail(LH_ERR_INVALID_ARG, "dweights needs Ys");
+    }
+    if (same_array(dYs, dY) || same_array(dYs, Ys)) return fail(LH_ERR_INVALID_ARG, "dYs must not alias an input");
     s = check_rows("dY", dY, dtype, c, ld_dy);
     if (s == LH_OK && dweights) s = check_rows("Ys", Ys, dtype, c, ld_ys);
     if (s == LH_OK && dYs) s = check_rows("dYs", dYs, dtype, c, ld_dys);
     if (s != LH_OK) return s;
-    if (n_tok == 0 || (c == 0 && !dweights)) return LH_OK;
+    if (n_tok == 0 || (no_rows && !dweights)) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
     const bool wide = wide_rows(dY, dtype, ld_dy) && (!dweights || wide_rows(Ys, dtype, ld_ys)) &&

@@ -967,9 +967,10 @@ lh_status check_weights(const uint8_t* W_packed, const uint8_t* W_scales, const 
                         int64_t n_groups, int64_t n_rows, int64_t c_out, int64_t c_in, const void* Y, lh_dtype out_dtype,
                         int64_t ld_y) {
     if (!valid_dtype(out_dtype)) return fail(LH_ERR_UNSUPPORTED, "out_dtype %d is not LH_BF16 or LH_F32", (int)out_dtype);
-    if (!W_packed || !W_scales || !W_gscale || !Y) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_rows < 0 || c_out < 0 || c_in < 0 || n_groups < 1)
         return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
+    if (n_rows > 0 && c_out > 0 && (!W_packed || !W_scales || !W_gscale || !Y))
+        return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (!offsets && n_groups != 1) return fail(LH_ERR_INVALID_ARG, "several groups need offsets");
     if (c_in % 32 != 0 || c_in == 0)
         return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a positive multiple of 32", (long long)c_in);
@@ -1008,11 +1009,10 @@ lh_status matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* 
     clear_error();
     lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
     if (s != LH_OK) return s;
-    if (!X_packed || !X_scales || !X_gscale) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (n_rows > 0 && c_out > 0 && (!X_packed || !X_scales || !X_gscale)) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned16(X_packed) || !aligned16(X_scales))
         return fail(LH_ERR_ALIGNMENT, "X_packed and X_scales must be 16-byte aligned");
-    if (Y == (const void*)X_packed || Y == (const void*)W_packed || Y == (const void*)X_scales ||
-        Y == (const void*)W_scales)
+    if (same_array(Y, X_packed) || same_array(Y, W_packed) || same_array(Y, X_scales) || same_array(Y, W_scales))
         return fail(LH_ERR_INVALID_ARG, "Y must not alias an input");
     if (n_rows == 0 || c_out == 0) return LH_OK;
     const int sms = sm_count();
@@ -1095,7 +1095,7 @@ extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_
     clear_error();
     lh_status s = check_weights(W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y, out_dtype, ld_y);
     if (s != LH_OK) return s;
-    if (Y == X || Y == (const void*)W_packed || Y == (const void*)W_scales || Y == workspace)
+    if (same_array(Y, X) || same_array(Y, W_packed) || same_array(Y, W_scales) || same_array(Y, workspace))
         return fail(LH_ERR_INVALID_ARG, "Y must not alias an input or the workspace");
     const size_t need = lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups);
     if (need > 0 && (!workspace || workspace_bytes < need))

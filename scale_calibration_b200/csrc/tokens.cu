@@ -251,9 +251,10 @@ lh_status check_tokens(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c
                        int64_t row_div, int64_t n_rows, const int64_t* offsets, int64_t n_groups, const uint8_t* packed,
                        const uint8_t* scale_tiles, const float* token_scale, const void* X_out, lh_dtype out_dtype) {
     if (!valid_dtype(x_dtype) || (X_out && !valid_dtype(out_dtype))) return fail(LH_ERR_UNSUPPORTED, "unknown dtype");
-    if (!X || !packed || !scale_tiles || !token_scale) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_src < 0 || n_rows < 0 || c_in < 0 || n_groups < 1)
         return fail(LH_ERR_INVALID_ARG, "sizes must be >= 0, n_groups >= 1");
+    if (n_rows > 0 && c_in > 0 && ((!X && n_src > 0) || !packed || !scale_tiles || !token_scale))
+        return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (row_div < 1) return fail(LH_ERR_INVALID_ARG, "row_div must be >= 1");
     if (n_rows > INT_MAX - 512 || n_groups > INT_MAX - 512)
         return fail(LH_ERR_UNSUPPORTED, "n_rows and n_groups must be below 2^31 - 512");
@@ -268,7 +269,7 @@ lh_status check_tokens(const void* X, lh_dtype x_dtype, int64_t n_src, int64_t c
     if (!aligned16(packed) || !aligned16(scale_tiles) || !aligned16(X_out))
         return fail(LH_ERR_ALIGNMENT, "packed, scale_tiles and X_out must be 16-byte aligned");
     if (c_in > (1 << 28)) return fail(LH_ERR_UNSUPPORTED, "c_in must be at most 2^28");  // a row of scale tiles: 2^31 bytes
-    if (X == X_out || X == (const void*)packed || X == (const void*)scale_tiles || packed == scale_tiles)
+    if (same_array(X, X_out) || same_array(X, packed) || same_array(X, scale_tiles) || same_array(packed, scale_tiles))
         return fail(LH_ERR_INVALID_ARG, "outputs must not alias X or one another");
     return LH_OK;
 }
@@ -291,11 +292,11 @@ extern "C" lh_status lh_nvfp4_tile_scales(const uint8_t* block_scales, int64_t n
                                           uint8_t* tiles, void* stream) {
     using namespace lh;
     clear_error();
-    if (!block_scales || !tiles) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
+    if (c_out != 0 && c_in != 0 && (!block_scales || !tiles)) return fail(LH_ERR_INVALID_ARG, "null pointer argument");
     if (n_mats < 1 || c_out < 0 || c_in < 0) return fail(LH_ERR_INVALID_ARG, "n_mats must be >= 1, sizes >= 0");
     if (c_in % 16 != 0) return fail(LH_ERR_UNSUPPORTED, "c_in=%lld is not a multiple of 16", (long long)c_in);
     if (!aligned16(tiles)) return fail(LH_ERR_ALIGNMENT, "tiles must be 16-byte aligned");
-    if (block_scales == tiles) return fail(LH_ERR_INVALID_ARG, "tiles must not alias block_scales");
+    if (same_array(block_scales, tiles)) return fail(LH_ERR_INVALID_ARG, "tiles must not alias block_scales");
     if (c_out == 0 || c_in == 0) return LH_OK;
     const int sms = sm_count();
     if (sms <= 0) return fail(LH_ERR_CUDA, "no CUDA device");

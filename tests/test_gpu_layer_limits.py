@@ -101,3 +101,26 @@ def test_rows_of_every_number_of_stages_one_after_another(cuda_ok, n, m, grouped
     for a, c, want, y in calls:
         assert torch.equal(y[:, :m].cpu(), want), c
     assert _lh().lh_nvfp4_status() == 0
+
+
+def test_a_bank_calibrated_without_tokens(cuda_ok):
+    lh = _lh()
+    W = torch.randn(3, 8, 64, device="cuda")
+    X = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    cal = lh.calibrate_routed(W, X, torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    assert (cal["codes"] == 1).all() and (cal["H"] == 0).all()  # H = 0: every code is as good, the lowest is taken
+    q = lh.QuantizedLayer(W, cal["global_amax"], cal["codes"])
+    r = lh.Routing(0, 2, 3).route(torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    assert r.offsets.tolist() == [0, 0, 0, 0] and q.forward_routed(X, r).shape == (0, 8)
+    one = lh.calibrate(W[0], X)
+    assert torch.equal(one["codes"][0], cal["codes"][0])
+
+
+def test_a_combination_without_rows_is_zero(cuda_ok):
+    lh = _lh()
+    pos = torch.full((6,), 3, dtype=torch.int32, device="cuda")  # past the end of no rows
+    rows, dy = torch.empty(0, 8, device="cuda"), torch.randn(3, 8, device="cuda")
+    y, dw = torch.full((3, 8), 5.0, device="cuda"), torch.full((3, 2), 5.0, device="cuda")
+    lh.lh_combine_tokens(rows, rows, 0, 8, 8, pos, None, 3, 2, y, 8)
+    lh.lh_combine_tokens_grad(dy, dy, 3, 2, 8, 8, rows, 8, 0, pos, None, rows, 8, dw)
+    assert (y == 0).all() and (dw == 0).all()

@@ -54,3 +54,38 @@ def test_linear_refuses_an_output_over_its_weights_or_workspace(n_rows):
         a["Y"] = a[y]
         assert lh.lh_nvfp4_linear(**a) == 1, y
         assert "alias" in lh.lh_last_error_message()
+
+
+def test_empty_calls_take_null_arrays():
+    # an empty tensor's pointer is NULL
+    lh = _lh()
+    t = lh.LH_BF16
+    assert lh.lh_gather_tokens(0, t, 0, 64, 64, 0, 2, 0, 0, 64, 0, False) == 0
+    assert lh.lh_gather_tokens(0, t, 0, 64, 64, FAKE, 2, 5, FAKE, 64, 0, False) == 0
+    assert lh.lh_gather_tokens(FAKE, t, 9, 64, 64, 0, 2, 0, 0, 64, 0, False) == 0
+    assert lh.lh_combine_tokens(0, t, 0, 64, 64, 0, None, 0, 2, 0, 64, 0, False) == 0
+    assert lh.lh_combine_tokens_grad(0, t, 0, 2, 64, 64, 0, 64, 0, 0, None, 0, 64, 0, 0, False) == 0
+    assert lh.lh_combine_tokens_grad(FAKE, t, 3, 2, 64, 64, 0, 64, 0, FAKE, None, 0, 64, 0, 0, False) == 0
+    for n_src, n_rows in ((0, 0), (9, 0)):
+        x = FAKE if n_src else 0
+        assert lh.lh_quantize_tokens(x, t, n_src, 64, 64, None, 1, n_rows, None, 1, None, 0, 0, 0, None, t, 0, False) == 0
+        assert lh.lh_nvfp4_linear(x, t, n_src, 64, 64, None, 1, n_rows, None, 1, None, FAKE, FAKE, FAKE, 8, 0, t, 8, 0, 0,
+                                  0, False) == 0
+    assert lh.lh_nvfp4_matmul(0, 0, 0, FAKE, FAKE, FAKE, None, 1, 0, 8, 64, 0, t, 8, 0, False) == 0
+    assert lh.lh_nvfp4_matmul(FAKE, FAKE, FAKE, 0, 0, FAKE, None, 1, 4, 0, 64, 0, t, 8, 0, False) == 0
+    assert lh.lh_nvfp4_tile_scales(0, 2, 0, 64, 0, 0, False) == 0
+    assert lh.lh_accumulate_hessian(0, t, 0, 64, 64, None, 1, FAKE, 0, 0, 0, False) == 0
+    assert lh.lh_accumulate_hessian_noalloc(0, t, 0, 64, 64, None, 1, FAKE, 0, False) == 0
+
+
+def test_null_arrays_that_have_elements_are_refused():
+    lh = _lh()
+    t = lh.LH_BF16
+    assert lh.lh_gather_tokens(0, t, 1, 64, 64, FAKE, 2, 5, FAKE, 64, 0, False) == 1
+    assert lh.lh_combine_tokens(FAKE, t, 4, 64, 64, FAKE, None, 1, 2, 0, 64, 0, False) == 1
+    assert lh.lh_combine_tokens(0, t, 4, 64, 64, FAKE, None, 1, 2, FAKE, 64, 0, False) == 1
+    assert lh.lh_combine_tokens_grad(FAKE, t, 1, 2, 64, 64, 0, 64, 4, FAKE, None, 0, 64, FAKE, 0, False) == 1
+    assert lh.lh_quantize_tokens(0, t, 1, 64, 64, None, 1, 1, None, 1, None, FAKE, FAKE + 4096, FAKE, None, t, 0, False) == 1
+    assert lh.lh_nvfp4_matmul(FAKE, FAKE, 0, FAKE, FAKE, FAKE, None, 1, 1, 8, 64, FAKE + 4096, t, 8, 0, False) == 1
+    assert lh.lh_nvfp4_tile_scales(0, 2, 1, 64, FAKE, 0, False) == 1
+    assert lh.lh_accumulate_hessian(0, t, 1, 64, 64, None, 1, FAKE, FAKE, 1 << 20, 0, False) == 1
