@@ -59,6 +59,8 @@ class Calibrator:
     def run(self, W, X, offsets=None, stream=None, zero_h: bool = True):
         import torch
         n_mats, c_out, c_in = self.n_mats, self.c_out, self.c_in
+        if X.dtype != torch.bfloat16:
+            raise ValueError(f"X must be bf16, not {X.dtype}")
         if self.Wq is None or self.Wq.dtype != (self.out_dtype or W.dtype):
             self.Wq = torch.empty(n_mats, c_out, c_in, dtype=self.out_dtype or W.dtype, device=W.device)
         if zero_h:
@@ -139,6 +141,8 @@ def calibrate_routed(W, X, expert_ids, out_dtype=None, stream=None):
     (bf16) and the experts that each was routed to (int32 [n_tok, k]): calibrate() on the sorted rows. Experts without
     tokens have H = 0 (every block gets code 1)."""
     import torch
+    if X.dtype != torch.bfloat16:
+        raise ValueError(f"X must be bf16, not {X.dtype}")
     _on_current_device(W=W, X=X, expert_ids=expert_ids)
     n_tok, k = expert_ids.shape
     if X.shape[0] != n_tok or X.shape[1] != W.shape[2]:
