@@ -61,6 +61,8 @@ class Calibrator:
         n_mats, c_out, c_in = self.n_mats, self.c_out, self.c_in
         if X.dtype != torch.bfloat16:
             raise ValueError(f"X must be bf16, not {X.dtype}")
+        if self.grouped:
+            _typed("offsets", offsets, torch.int64, self.n_groups + 1)
         if self.Wq is None or self.Wq.dtype != (self.out_dtype or W.dtype):
             self.Wq = torch.empty(n_mats, c_out, c_in, dtype=self.out_dtype or W.dtype, device=W.device)
         if zero_h:
@@ -90,6 +92,12 @@ def _on_current_device(**tensors):
     for name, t in tensors.items():
         if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _typed(name, t, dtype, n):
+    """The library is given addresses: t has to begin with n values of this type, one after another."""
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values of {dtype}, not {tuple(t.shape)} of {t.dtype}")
 
 
 def _on(stream):
@@ -159,20 +167,25 @@ def calibrate_routed(W, X, expert_ids, out_dtype=None, stream=None):
 class QuantizedLayer:
     """A calibrated layer in NVFP4, run with NVFP4 tokens (W4A4): Y = Xq Wq^T.
 
-    W [n_mats, c_out, c_in] (or one matrix [c_out, c_in]), global_amax and codes as `calibrate` returns them;
-    x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None for one scale per token. The packed
-    weights and their scale tiles are made once; every call has a workspace of its own from torch's allocator, so calls
-    on several streams and captured graphs do not share one."""
+    W [n_mats, c_out, c_in] (or one matrix [c_out, c_in]), global_amax (f32 [n_mats]) and codes (uint8 [n_mats, c_out,
+    c_in / 16]) as `calibrate` returns them; x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None
+    for one scale per token. The packed weights and their scale tiles are made once; every call has a workspace of its own
+    from torch's allocator, so calls on several streams and captured graphs do not share one."""
 
     def __init__(self, W, global_amax, codes, x_amax=None, stream=None):
         import torch
         if W.dim() == 2:
             W = W.unsqueeze(0)
-        _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
         self.n_mats, self.c_out, self.c_in = W.shape
         if self.c_in % 32:
             raise ValueError(f"c_in={self.c_in} is not a multiple of 32")
         J = self.c_in // 16
+        _typed("global_amax", global_amax, torch.float32, self.n_mats)
+        if codes.dtype != torch.uint8 or codes.numel() != self.n_mats * self.c_out * J:
+            raise ValueError(f"codes must be uint8 [{self.n_mats}, {self.c_out}, {J}], not {tuple(codes.shape)} of {codes.dtype}")
+        if x_amax is not None:
+            _typed("x_amax", x_amax, torch.float32, 1)
+        _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
         with _on(stream):
             codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
             W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
@@ -208,8 +221,11 @@ class QuantizedLayer:
     def forward(self, X, offsets=None, out_dtype=None, stream=None):
         """Y [n_tok, c_out] of X [n_tok, c_in]; with several matrices the tokens of each are those of its group
         (offsets int64 [n_mats + 1] on the device); rows of tokens in no group are left unset."""
+        import torch
         if (offsets is None) != (self.n_mats == 1):
             raise ValueError("several matrices need offsets, and one takes none")
+        if offsets is not None:
+            _typed("offsets", offsets, torch.int64, self.n_mats + 1)
         with _on(stream):
             return self._linear(X, None, 1, X.shape[0], offsets, out_dtype)
 

@@ -21,3 +21,33 @@ def test_calibration_takes_bf16_tokens_only(dtype):
     cal = lh.Calibrator(1, 8, 64, 10, False, device="cpu")
     with pytest.raises(ValueError, match="X must be bf16"):
         cal.run(W[:1], X)
+
+
+def parts(n_mats=3, c_out=8, c_in=64):
+    return dict(W=torch.zeros(n_mats, c_out, c_in), global_amax=torch.ones(n_mats),
+                codes=torch.ones(n_mats, c_out, c_in // 16, dtype=torch.uint8), x_amax=None)
+
+
+@pytest.mark.parametrize("over,what", [
+    (dict(codes=torch.ones(3, 8, 4, dtype=torch.int32)), "codes"), (dict(codes=torch.ones(3, 8, 3, dtype=torch.uint8)), "codes"),
+    (dict(codes=torch.ones(3, 8, 4)), "codes"), (dict(global_amax=torch.ones(3).double()), "global_amax"),
+    (dict(global_amax=torch.ones(3).bfloat16()), "global_amax"), (dict(global_amax=torch.ones(2)), "global_amax"),
+    (dict(global_amax=torch.ones(6)[::2]), "global_amax"), (dict(x_amax=torch.ones(1).bfloat16()), "x_amax"),
+    (dict(x_amax=torch.ones(1).double()), "x_amax"), (dict(x_amax=torch.ones(0)), "x_amax"),
+])
+def test_a_layer_refuses_other_types_and_sizes(over, what):
+    with pytest.raises(ValueError, match=what):
+        _lh().QuantizedLayer(**dict(parts(), **over))
+
+
+@pytest.mark.parametrize("offsets", [torch.zeros(4, dtype=torch.int32), torch.zeros(3, dtype=torch.int64), torch.zeros(4),
+                                     torch.zeros(8, dtype=torch.int64)[::2]])
+def test_offsets_of_other_types_and_sizes_are_refused(offsets):
+    # they would be read past their end
+    lh = _lh()
+    layer = object.__new__(lh.QuantizedLayer)
+    layer.n_mats, layer.c_out, layer.c_in, layer.x_amax, layer.packed = 3, 8, 64, None, torch.zeros(1)
+    with pytest.raises(ValueError, match="offsets must be 4"):
+        layer(torch.zeros(5, 64), offsets)
+    with pytest.raises(ValueError, match="offsets must be 4"):
+        lh.Calibrator(3, 8, 64, 5, True, device="cpu").run(torch.zeros(3, 8, 64), torch.zeros(5, 64).bfloat16(), offsets)
