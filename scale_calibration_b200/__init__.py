@@ -100,6 +100,14 @@ def _typed(name, t, dtype, n):
         raise ValueError(f"{name} must be {n} contiguous values of {dtype}, not {tuple(t.shape)} of {t.dtype}")
 
 
+def _no_gradient(**tensors):
+    """The results are not part of autograd's graph: a gradient would be lost without a word."""
+    import torch
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which an NVFP4 layer does not give: call it under torch.no_grad()")
+
+
 def _on(stream):
     """Makes `stream` (a torch stream, its handle, or None for the current one) current, so that what is allocated for
     its kernels is not handed out again before they are done."""
@@ -170,7 +178,8 @@ class QuantizedLayer:
     W [n_mats, c_out, c_in] (or one matrix [c_out, c_in]), global_amax (f32 [n_mats]) and codes (uint8 [n_mats, c_out,
     c_in / 16]) as `calibrate` returns them; x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None
     for one scale per token. The packed weights and their scale tiles are made once; every call has a workspace of its own
-    from torch's allocator, so calls on several streams and captured graphs do not share one."""
+    from torch's allocator, so calls on several streams and captured graphs do not share one. There is no backward pass:
+    tokens or weights of the combination that require a gradient are refused outside torch.no_grad()."""
 
     def __init__(self, W, global_amax, codes, x_amax=None, stream=None):
         import torch
@@ -224,6 +233,7 @@ class QuantizedLayer:
         import torch
         if (offsets is None) != (self.n_mats == 1):
             raise ValueError("several matrices need offsets, and one takes none")
+        _no_gradient(X=X)
         if offsets is not None:
             _typed("offsets", offsets, torch.int64, self.n_mats + 1)
         with _on(stream):
@@ -240,6 +250,7 @@ class QuantizedLayer:
             raise ValueError("the routing is for another number of tokens or experts")
         if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (n_tok, k)):
             raise ValueError(f"weights must be f32 [{n_tok}, {k}]")
+        _no_gradient(X=X, weights=weights)
         _on_current_device(weights=weights)
         with _on(stream):
             rows = self._linear(X, routing.order, k, n_tok * k, routing.offsets, out_dtype)

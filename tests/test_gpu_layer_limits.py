@@ -124,3 +124,18 @@ def test_a_combination_without_rows_is_zero(cuda_ok):
     lh.lh_combine_tokens(rows, rows, 0, 8, 8, pos, None, 3, 2, y, 8)
     lh.lh_combine_tokens_grad(dy, dy, 3, 2, 8, 8, rows, 8, 0, pos, None, rows, 8, dw)
     assert (y == 0).all() and (dw == 0).all()
+
+
+def test_a_layer_runs_on_detached_tokens(cuda_ok):
+    lh = _lh()
+    W = torch.randn(3, 8, 64, device="cuda")
+    cal = lh.calibrate_routed(W, torch.randn(9, 64, device="cuda").bfloat16(), torch.zeros(9, 2, dtype=torch.int32, device="cuda"))
+    q = lh.QuantizedLayer(W, cal["global_amax"], cal["codes"])
+    x = torch.randn(9, 64, device="cuda", requires_grad=True)
+    w = torch.rand(9, 2, device="cuda", requires_grad=True)
+    r = lh.Routing(9, 2, 3).route(torch.arange(18, dtype=torch.int32, device="cuda").view(9, 2) % 3)
+    with pytest.raises(ValueError):
+        q.forward_routed(x, r, w)
+    with torch.no_grad():
+        y = q.forward_routed(x, r, w)
+    assert torch.equal(y, q.forward_routed(x.detach(), r, w.detach())) and not y.requires_grad

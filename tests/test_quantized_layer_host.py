@@ -51,3 +51,18 @@ def test_offsets_of_other_types_and_sizes_are_refused(offsets):
         layer(torch.zeros(5, 64), offsets)
     with pytest.raises(ValueError, match="offsets must be 4"):
         lh.Calibrator(3, 8, 64, 5, True, device="cpu").run(torch.zeros(3, 8, 64), torch.zeros(5, 64).bfloat16(), offsets)
+
+
+def test_a_layer_refuses_to_lose_a_gradient():
+    lh = _lh()
+    one, bank = (object.__new__(lh.QuantizedLayer) for _ in range(2))
+    for layer, n_mats in ((one, 1), (bank, 3)):
+        layer.n_mats, layer.c_out, layer.c_in, layer.x_amax, layer.packed = n_mats, 8, 64, None, torch.zeros(1)
+    x = torch.zeros(5, 64, requires_grad=True)
+    off = torch.zeros(4, dtype=torch.int64)
+    w = torch.ones(5, 2, requires_grad=True)
+    routing = lh.Routing(5, 2, 3, device="cpu")
+    for call in (lambda: one(x), lambda: bank(x, off), lambda: bank.forward_routed(x, routing),
+                 lambda: bank.forward_routed(x.detach(), routing, w)):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
