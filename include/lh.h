@@ -449,13 +449,18 @@ LH_API lh_status lh_quantize_tokens(const void* X, lh_dtype x_dtype, int64_t n_s
  *   2^31 - 512.
  * Waits inside the kernel are bounded (1 s). One that gives up leaves Y incomplete and
  * is reported by lh_nvfp4_status, which synchronises `stream`, returns LH_ERR_TIMEOUT
- * if that happened on the current device since the last call, and clears it.
+ * if that happened on the current device since the last call, and clears it: one word
+ * per device, for the products of all streams and callers.
+ * lh_debug_nvfp4_wait_timeout (diagnostics) runs such a wait on a barrier that nothing
+ * arrives on (arrive == 0) or that is completed first, with a limit of timeout_us
+ * (1 .. 1e6) microseconds, and reports it in the same way.
  * ---------------------------------------------------------------------- */
 LH_API lh_status lh_nvfp4_matmul(const uint8_t* X_packed, const uint8_t* X_scales, const float* X_gscale,
                                  const uint8_t* W_packed, const uint8_t* W_scales, const float* W_gscale,
                                  const int64_t* offsets, int64_t n_groups, int64_t n_rows, int64_t c_out,
                                  int64_t c_in, void* Y, lh_dtype out_dtype, int64_t ld_y, void* stream);
 LH_API lh_status lh_nvfp4_status(void* stream);
+LH_API lh_status lh_debug_nvfp4_wait_timeout(int64_t timeout_us, int arrive, void* stream);
 
 /* ------------------------------------------------------------------------
  * lh_quantize_tokens and lh_nvfp4_matmul in one call: Y = Xq Wq^T from the tokens

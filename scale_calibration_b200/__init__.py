@@ -25,6 +25,7 @@ from ._binding import (  # noqa: F401
     lh_probe_fma, lh_probe_fma_flop,
     lh_route_tokens, lh_gather_tokens, lh_combine_tokens, lh_combine_tokens_grad, lh_quantize_tokens,
     lh_nvfp4_weight_scale_bytes, lh_nvfp4_token_scale_bytes, lh_nvfp4_tile_scales, lh_nvfp4_matmul, lh_nvfp4_status,
+    lh_debug_nvfp4_wait_timeout,
     lh_nvfp4_linear_workspace_bytes, lh_nvfp4_linear,
 )
 
@@ -179,7 +180,8 @@ class QuantizedLayer:
     c_in / 16]) as `calibrate` returns them; x_amax: the calibrated amax of the activations (f32 CUDA tensor [1]), or None
     for one scale per token. The packed weights and their scale tiles are made once; every call has a workspace of its own
     from torch's allocator, so calls on several streams and captured graphs do not share one. There is no backward pass:
-    tokens or weights of the combination that require a gradient are refused outside torch.no_grad()."""
+    tokens or weights of the combination that require a gradient are refused outside torch.no_grad(). The products' waits
+    are bounded: a GPU that stops answering for a second leaves results incomplete, which `check` reports."""
 
     def __init__(self, W, global_amax, codes, x_amax=None, stream=None):
         import torch
@@ -208,6 +210,13 @@ class QuantizedLayer:
                               self.block_scales, self.global_scale)
             lh_nvfp4_tile_scales(self.block_scales, self.n_mats, self.c_out, self.c_in, self.scale_tiles)
         self.x_amax = x_amax
+
+    @staticmethod
+    def check(stream=None):
+        """Waits for `stream` and raises LHError if a product on the current device, of any layer, has given up a wait
+        since the last look: results since then may be incomplete."""
+        from ._binding import _check
+        _check(lh_nvfp4_status(stream), "lh_nvfp4_status")
 
     def _linear(self, X, rows, row_div, n_rows, offsets, out_dtype):
         import torch

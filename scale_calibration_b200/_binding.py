@@ -24,7 +24,7 @@ EXPORTS = [
     "lh_search_amax", "lh_sweep_workspace_bytes", "lh_sweep_scales_ws", "lh_probe_fma", "lh_probe_fma_flop", "lh_debug_sweep_counts",
     "lh_route_tokens", "lh_gather_tokens", "lh_combine_tokens", "lh_combine_tokens_grad",
     "lh_nvfp4_weight_scale_bytes", "lh_nvfp4_token_scale_bytes", "lh_nvfp4_tile_scales", "lh_quantize_tokens",
-    "lh_nvfp4_matmul", "lh_nvfp4_status", "lh_nvfp4_linear_workspace_bytes", "lh_nvfp4_linear",
+    "lh_nvfp4_matmul", "lh_nvfp4_status", "lh_debug_nvfp4_wait_timeout", "lh_nvfp4_linear_workspace_bytes", "lh_nvfp4_linear",
 ]
 LH_SCALE_MAX, LH_SCALE_FOUR_OVER_SIX, LH_SCALE_MSE = range(3)
 
@@ -70,6 +70,7 @@ def _load() -> ctypes.CDLL:
         "lh_quantize_tokens": (I32, [P, I32, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, P, I32, P]),
         "lh_nvfp4_matmul": (I32, [P, P, P, P, P, P, P, I64, I64, I64, I64, P, I32, I64, P]),
         "lh_nvfp4_status": (I32, [P]),
+        "lh_debug_nvfp4_wait_timeout": (I32, [I64, I32, P]),
         "lh_nvfp4_linear_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
         "lh_nvfp4_linear": (I32, [P, I32, I64, I64, I64, P, I64, I64, P, I64, P, P, P, P, I64, P, I32, I64, P,
                                   ctypes.c_size_t, P]),
@@ -339,6 +340,13 @@ def lh_nvfp4_matmul(X_packed, X_scales, X_gscale, W_packed, W_scales, W_gscale, 
 
 def lh_nvfp4_status(stream=None) -> int:
     return _lib.lh_nvfp4_status(_stream(stream))
+
+
+def lh_debug_nvfp4_wait_timeout(timeout_us, arrive, stream=None, check=True) -> int:
+    s = _lib.lh_debug_nvfp4_wait_timeout(timeout_us, arrive, _stream(stream))
+    if check:
+        _check(s, "lh_debug_nvfp4_wait_timeout")
+    return s
 
 
 def lh_nvfp4_linear_workspace_bytes(n_rows, c_in, n_groups) -> int:

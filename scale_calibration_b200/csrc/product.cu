@@ -145,15 +145,16 @@ struct Walk {
     }
 };
 
-// Waits for the phase of `parity`; false after 1 s, or when another warp gave up. The timer
+// Waits for the phase of `parity`; false after `limit` (1 s), or when another warp gave up. The timer
 // is read only after many tries: reading it takes longer than most waits.
-__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint64_t limit = kTimeoutNs) {
     uint64_t t0 = 0;
     for (uint32_t it = 1; !mbar_try(bar, parity); ++it) {
         if ((it & 255) != 0) continue;
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
-        if (*abort_flag || now - t0 > kTimeoutNs) return false;
+        if (*abort_flag || now - t0 > limit) return false;
     }
     return true;
 }
@@ -164,6 +165,20 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void give_up(volatile int* flag) {
     *flag = 1;
     atomicExch(&product_status, (unsigned)LH_ERR_TIMEOUT);
+}
+
+// That wait and its report on a barrier that nothing arrives on (arrive == 0), or that is completed first.
+__global__ void product_wait_kernel(uint64_t limit, int arrive) {
+    __shared__ uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar), 1);
+        abort_flag = 0;
+        mbar_init_fence();
+    }
+    __syncthreads();
+    if (arrive && threadIdx.x == 0) mbar_arrive(smem_u32(&bar));
+    if (!__all_sync(0xFFFFFFFFu, lane_wait(smem_u32(&bar), 0, &abort_flag, limit))) give_up(&abort_flag);
 }
 
 __device__ __forceinline__ void store_out(float* y, float v) { *y = v; }
@@ -1125,6 +1140,15 @@ extern "C" lh_status lh_nvfp4_linear(const void* X, lh_dtype x_dtype, int64_t n_
     // the quantisation, if it ran, waited for everything before it and writes the workspace alone
     return matmul(packed, scales, gscale, W_packed, W_scales, W_gscale, offsets, n_groups, n_rows, c_out, c_in, Y,
                   out_dtype, ld_y, n_src > 0, stream);
+}
+
+extern "C" lh_status lh_debug_nvfp4_wait_timeout(int64_t timeout_us, int arrive, void* stream) {
+    using namespace lh;
+    clear_error();
+    if (timeout_us < 1 || timeout_us > 1000000) return fail(LH_ERR_INVALID_ARG, "timeout_us must be in [1, 1e6]");
+    if (sm_count() <= 0) return fail(LH_ERR_CUDA, "no CUDA device");
+    product_wait_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>((uint64_t)timeout_us * 1000ull, arrive);
+    return cuda_status(cudaGetLastError(), "product_wait_kernel launch");
 }
 
 extern "C" lh_status lh_nvfp4_status(void* stream) {

@@ -139,3 +139,29 @@ def test_a_layer_runs_on_detached_tokens(cuda_ok):
     with torch.no_grad():
         y = q.forward_routed(x, r, w)
     assert torch.equal(y, q.forward_routed(x.detach(), r, w.detach())) and not y.requires_grad
+
+
+def test_a_layer_reports_an_expired_wait(cuda_ok):
+    lh = _lh()
+    W = torch.randn(8, 64, device="cuda")
+    cal = lh.calibrate(W, torch.randn(40, 64, device="cuda").bfloat16())
+    q = lh.QuantizedLayer(W, cal["global_amax"], cal["codes"])
+    x = torch.randn(300, 64, device="cuda")
+    y = q(x)
+    q.check()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    lh.lh_debug_nvfp4_wait_timeout(50000, 0)  # 50 ms, nothing arrives
+    end.record()
+    with pytest.raises(lh.LHError, match="LH_ERR_TIMEOUT") as e:
+        q.check()
+    assert e.value.status == 6 and 45 <= start.elapsed_time(end) <= 500
+    q.check()  # told once
+    lh.lh_debug_nvfp4_wait_timeout(50000, 1)  # completed: nothing to tell
+    q.check()
+    s = torch.cuda.Stream()
+    lh.lh_debug_nvfp4_wait_timeout(1000, 0, s)
+    with pytest.raises(lh.LHError):
+        q.check(s)
+    assert torch.equal(q(x), y)
+    q.check()

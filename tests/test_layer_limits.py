@@ -89,3 +89,9 @@ def test_null_arrays_that_have_elements_are_refused():
     assert lh.lh_nvfp4_matmul(FAKE, FAKE, 0, FAKE, FAKE, FAKE, None, 1, 1, 8, 64, FAKE + 4096, t, 8, 0, False) == 1
     assert lh.lh_nvfp4_tile_scales(0, 2, 1, 64, FAKE, 0, False) == 1
     assert lh.lh_accumulate_hessian(0, t, 1, 64, 64, None, 1, FAKE, FAKE, 1 << 20, 0, False) == 1
+
+
+def test_wait_probe_refusals():
+    lh = _lh()
+    for us in (0, -1, 1000001):
+        assert lh.lh_debug_nvfp4_wait_timeout(us, 0, 0, False) == 1
