@@ -3,7 +3,7 @@
 Every function here has the name of the C entry point it calls and takes
 device pointers either as torch CUDA tensors or as integers. Nothing here
 computes any part of the calibration: all arithmetic runs in the library's
-kernels. If liblh.so (or _lhcall.so, see csrc/pycall.c) is missing the import
+kernels. If liblh.so (or _lhcall, see csrc/pycall.c) is missing the import
 fails; there is no fallback.
 """
 from __future__ import annotations

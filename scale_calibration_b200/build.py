@@ -1,5 +1,5 @@
 """Builds liblh.so (the CUDA library behind include/lh.h) for sm_100a, and the
-small CPython extension that calls it (_lhcall.so).
+small CPython extension that calls it (_lhcall).
 
     python scale_calibration_b200/build.py [--verbose] [--counters]
 
@@ -31,12 +31,16 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-# The Python side's call path (csrc/pycall.c), a plain CPython extension.
+# The Python side's call path (csrc/pycall.c), a plain CPython extension. Its name carries
+# the interpreter's ABI, so that another interpreter does not load it.
 CALL_SRC = os.path.join(CSRC, "pycall.c")
-CALL_LIB = os.path.join(PKG, "_lhcall.so")
+CALL_LIB = os.path.join(PKG, "_lhcall" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALL_LIB_UNTAGGED = os.path.join(PKG, "_lhcall.so")  # what earlier builds left: any interpreter would load it
 
 
 def build_call(force: bool = False) -> str:
+    if os.path.exists(CALL_LIB_UNTAGGED):
+        os.remove(CALL_LIB_UNTAGGED)
     if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < os.path.getmtime(CALL_SRC):
         tmp = CALL_LIB + f".tmp{os.getpid()}"
         subprocess.check_call([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-fPIC", "-shared", "-fvisibility=hidden",
