@@ -41,10 +41,14 @@ CALL_LIB_UNTAGGED = os.path.join(PKG, "_lhcall.so")  # what earlier builds left:
 def build_call(force: bool = False) -> str:
     if os.path.exists(CALL_LIB_UNTAGGED):
         os.remove(CALL_LIB_UNTAGGED)
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print(f"no Python.h in {include}: built without {os.path.basename(CALL_LIB)}, calls go through ctypes", file=sys.stderr)
+        return ""
     if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < os.path.getmtime(CALL_SRC):
         tmp = CALL_LIB + f".tmp{os.getpid()}"
         subprocess.check_call([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-fPIC", "-shared", "-fvisibility=hidden",
-                               "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp])
+                               "-I", include, CALL_SRC, "-o", tmp])
         os.replace(tmp, CALL_LIB)
     return CALL_LIB
 
