@@ -111,7 +111,7 @@ def _no_gradient(**tensors):
 
 def _on(stream):
     """Makes `stream` (a torch stream, its handle, or None for the current one) current, so that what is allocated for
-    its kernels is not handed out again before they are done."""
+    its kernels is not handed out again before they are done. Its device becomes the current one: tensors are checked after."""
     import contextlib
     import torch
     if stream is None:
@@ -147,8 +147,8 @@ class Routing:
         import torch
         if expert_ids.dtype != torch.int32 or tuple(expert_ids.shape) != (self.n_tok, self.k):
             raise ValueError(f"expert_ids must be int32 [{self.n_tok}, {self.k}]")
-        _on_current_device(expert_ids=expert_ids, offsets=self.offsets)
         with _on(stream):
+            _on_current_device(expert_ids=expert_ids, offsets=self.offsets)
             lh_route_tokens(expert_ids.contiguous(), self.n_tok, self.k, self.n_experts, self.offsets, self.order, self.pos)
         return self
 
@@ -160,11 +160,11 @@ def calibrate_routed(W, X, expert_ids, out_dtype=None, stream=None):
     import torch
     if X.dtype != torch.bfloat16:
         raise ValueError(f"X must be bf16, not {X.dtype}")
-    _on_current_device(W=W, X=X, expert_ids=expert_ids)
     n_tok, k = expert_ids.shape
     if X.shape[0] != n_tok or X.shape[1] != W.shape[2]:
         raise ValueError("X must be [n_tok, c_in]")
     with _on(stream):
+        _on_current_device(W=W, X=X, expert_ids=expert_ids)
         X = _rows(X, "X")
         r = Routing(n_tok, k, W.shape[0], W.device).route(expert_ids)
         # rows of slots without an expert lie behind the last group and are never used
@@ -196,8 +196,8 @@ class QuantizedLayer:
             raise ValueError(f"codes must be uint8 [{self.n_mats}, {self.c_out}, {J}], not {tuple(codes.shape)} of {codes.dtype}")
         if x_amax is not None:
             _typed("x_amax", x_amax, torch.float32, 1)
-        _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
         with _on(stream):
+            _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
             codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
             W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
             dev = W.device
@@ -260,8 +260,8 @@ class QuantizedLayer:
         if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (n_tok, k)):
             raise ValueError(f"weights must be f32 [{n_tok}, {k}]")
         _no_gradient(X=X, weights=weights)
-        _on_current_device(weights=weights)
         with _on(stream):
+            _on_current_device(weights=weights, routing=routing.pos)
             rows = self._linear(X, routing.order, k, n_tok * k, routing.offsets, out_dtype)
             Y = torch.empty(n_tok, rows.stride(0), dtype=rows.dtype, device=X.device)[:, :self.c_out]
             if n_tok == 0:

@@ -66,3 +66,37 @@ def test_a_layer_refuses_to_lose_a_gradient():
                  lambda: bank.forward_routed(x.detach(), routing, w)):
         with pytest.raises(ValueError, match="requires a gradient"):
             call()
+
+
+class OnGPU0(torch.Tensor):
+    """Says that it is on the first GPU."""
+    is_cuda = True
+    device = torch.device("cuda:0")
+
+
+def test_tensors_have_to_be_on_the_streams_device(monkeypatch):
+    # a stream makes its device the current one: tensors of the device that was current before are not there
+    import contextlib
+    lh = _lh()
+    current = [0]
+
+    @contextlib.contextmanager
+    def on(stream):
+        current[0] = 1
+        yield
+        current[0] = 0
+
+    monkeypatch.setattr(lh, "_on", on)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    gpu0 = lambda t: t.as_subclass(OnGPU0)  # noqa: E731
+    ids = gpu0(torch.zeros(10, 2, dtype=torch.int32))
+    routing = lh.Routing(10, 2, 3, device="cpu")
+    routing.pos = gpu0(routing.pos)
+    layer = object.__new__(lh.QuantizedLayer)
+    layer.n_mats = 3
+    w = gpu0(torch.ones(10, 2))
+    for call in (lambda: lh.QuantizedLayer(**{k: v if v is None else gpu0(v) for k, v in parts().items()}),
+                 lambda: routing.route(ids), lambda: layer.forward_routed(gpu0(torch.zeros(10, 64)), routing, w),
+                 lambda: lh.calibrate_routed(gpu0(torch.zeros(3, 8, 64)), gpu0(torch.zeros(10, 64).bfloat16()), ids)):
+        with pytest.raises(ValueError, match="is on cuda:0, the current device is cuda:1"):
+            call()
