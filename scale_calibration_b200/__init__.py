@@ -64,6 +64,7 @@ class Calibrator:
             raise ValueError(f"X must be bf16, not {X.dtype}")
         if self.grouped:
             _typed("offsets", offsets, torch.int64, self.n_groups + 1)
+        W, X = _matrices(W), _rows(X, "X")
         if self.Wq is None or self.Wq.dtype != (self.out_dtype or W.dtype):
             self.Wq = torch.empty(n_mats, c_out, c_in, dtype=self.out_dtype or W.dtype, device=W.device)
         if zero_h:
@@ -129,6 +130,13 @@ def _rows(t, what):
         return t
     out = torch.empty(t.shape[0], -(-max(t.shape[1], 1) // per) * per, dtype=t.dtype, device=t.device)[:, :t.shape[1]]
     return out.copy_(t)
+
+
+def _matrices(W):
+    """W [n_mats, c_out, c_in] (or one matrix) as rows at one distance, matrix after matrix: copied if it does not lie so."""
+    if W.stride(-1) == 1 and (W.dim() == 2 or W.shape[0] == 1 or W.stride(0) == W.stride(1) * W.shape[1]):
+        return W
+    return W.contiguous()
 
 
 class Routing:
@@ -199,7 +207,7 @@ class QuantizedLayer:
         with _on(stream):
             _on_current_device(W=W, global_amax=global_amax, codes=codes, x_amax=x_amax)
             codes = codes.reshape(self.n_mats, self.c_out, J).contiguous()
-            W = W if W.stride(2) == 1 and W.stride(0) == W.stride(1) * self.c_out else W.contiguous()
+            W = _matrices(W)
             dev = W.device
             self.packed = torch.empty(self.n_mats, self.c_out, self.c_in // 2, dtype=torch.uint8, device=dev)
             self.block_scales = torch.empty_like(codes)

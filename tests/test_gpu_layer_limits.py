@@ -165,3 +165,26 @@ def test_a_layer_reports_an_expired_wait(cuda_ok):
         q.check(s)
     assert torch.equal(q(x), y)
     q.check()
+
+
+def test_calibration_of_tensors_that_lie_otherwise(cuda_ok):
+    # every other expert of a bank, transposed weights, transposed and unaligned tokens: the same as their copies
+    lh = _lh()
+    W = torch.randn(6, 16, 64, device="cuda")
+    X = torch.randn(40, 64, device="cuda").bfloat16()
+    ids = (torch.arange(80, device="cuda").view(40, 2) % 3).to(torch.int32)
+    wide = torch.zeros(40, 69, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:67] = X
+    turned = W[::2].transpose(1, 2).contiguous().transpose(1, 2)
+    want = lh.calibrate_routed(W[::2].contiguous(), X, ids)
+    for w in (W[::2], turned, W[1::2].clone().copy_(W[::2])):
+        for x in (X, X.t().contiguous().t(), wide[:, 3:67]):
+            got = lh.calibrate_routed(w, x, ids)
+            assert all(torch.equal(got[key], want[key]) for key in want)
+    want = lh.calibrate(W[1].contiguous(), X)
+    for x in (X.t().contiguous().t(), wide[:, 3:67]):
+        got = lh.calibrate(W.transpose(1, 2).contiguous().transpose(1, 2)[1], x)
+        assert all(torch.equal(got[key], want[key]) for key in want)
+    bank = lh.calibrate_routed(W[::2], X, ids)
+    a, b = (lh.QuantizedLayer(w, bank["global_amax"], bank["codes"]) for w in (W[::2], turned))
+    assert torch.equal(a.packed, b.packed) and torch.equal(a.scale_tiles, b.scale_tiles)
