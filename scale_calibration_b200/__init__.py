@@ -117,7 +117,9 @@ def _on(stream):
     import torch
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):  # 0 and 1 name the default stream; ExternalStream(0) would be a new one
+        stream = torch.cuda.ExternalStream(stream) if stream > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _rows(t, what):

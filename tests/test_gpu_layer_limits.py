@@ -188,3 +188,25 @@ def test_calibration_of_tensors_that_lie_otherwise(cuda_ok):
     bank = lh.calibrate_routed(W[::2], X, ids)
     a, b = (lh.QuantizedLayer(w, bank["global_amax"], bank["codes"]) for w in (W[::2], turned))
     assert torch.equal(a.packed, b.packed) and torch.equal(a.scale_tiles, b.scale_tiles)
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_streams_handle_is_the_default_stream(cuda_ok, handle):
+    # work that waits on the default stream comes before a call with its handle
+    lh = _lh()
+    W = torch.randn(3, 8, 64, device="cuda")
+    X = torch.randn(9, 64, device="cuda").bfloat16()
+    ids = (torch.arange(18, device="cuda").view(9, 2) % 3).to(torch.int32)
+    want = lh.calibrate_routed(W, X, ids)
+    q = lh.QuantizedLayer(W, want["global_amax"], want["codes"])
+    r = lh.Routing(9, 2, 3).route(ids)
+    y = q.forward_routed(X, r)
+    x, i, w = torch.zeros_like(X), torch.zeros_like(ids), torch.zeros_like(W)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second
+    x.copy_(X), i.copy_(ids), w.copy_(W)
+    got = lh.calibrate_routed(w, x, i, stream=handle)
+    q2 = lh.QuantizedLayer(w, got["global_amax"], got["codes"], stream=handle)
+    y2 = q2.forward_routed(x, lh.Routing(9, 2, 3).route(i, stream=handle), stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and all(torch.equal(got[key], want[key]) for key in want)
