@@ -32,7 +32,7 @@ from ._binding import (  # noqa: F401
 
 class Calibrator:
     """Device buffers for calibrating one layer shape; `run` launches the
-    whole hot path on the current stream. Inputs are torch CUDA tensors:
+    whole hot path on the current stream, or on the one that it is given. Inputs are torch CUDA tensors:
     W [n_mats, c_out, c_in] (bf16 or f32), X [n_tok, c_in] bf16, optional
     offsets int64 [n_mats + 1] on the device (one token group per matrix)."""
 
@@ -64,17 +64,18 @@ class Calibrator:
             raise ValueError(f"X must be bf16, not {X.dtype}")
         if self.grouped:
             _typed("offsets", offsets, torch.int64, self.n_groups + 1)
-        W, X = _matrices(W), _rows(X, "X")
-        if self.Wq is None or self.Wq.dtype != (self.out_dtype or W.dtype):
-            self.Wq = torch.empty(n_mats, c_out, c_in, dtype=self.out_dtype or W.dtype, device=W.device)
-        if zero_h:
-            self.H.zero_()
-        lh_absmax(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax, stream)
-        lh_accumulate_hessian(X, LH_BF16, X.shape[0], c_in, X.stride(0), offsets if self.grouped else None,
-                              self.n_groups, self.H, self.ws, self.ws_bytes, stream)
-        lh_sweep_scales_ws(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax, self.H, self.best_amax,
-                           self.best_code, self.sweep_ws, self.sweep_ws_bytes, stream)
-        lh_fake_quant(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax, self.best_code, self.Wq, self.Wq, stream)
+        with _on(stream):
+            W, X = _matrices(W), _rows(X, "X")
+            if self.Wq is None or self.Wq.dtype != (self.out_dtype or W.dtype):
+                self.Wq = torch.empty(n_mats, c_out, c_in, dtype=self.out_dtype or W.dtype, device=W.device)
+            if zero_h:
+                self.H.zero_()
+            lh_absmax(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax)
+            lh_accumulate_hessian(X, LH_BF16, X.shape[0], c_in, X.stride(0), offsets if self.grouped else None,
+                                  self.n_groups, self.H, self.ws, self.ws_bytes)
+            lh_sweep_scales_ws(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax, self.H, self.best_amax,
+                               self.best_code, self.sweep_ws, self.sweep_ws_bytes)
+            lh_fake_quant(W, W, n_mats, c_out, c_in, W.stride(-2), self.amax, self.best_code, self.Wq, self.Wq)
         return self.best_code, self.best_amax, self.Wq
 
 
@@ -82,9 +83,10 @@ def calibrate(W, X, offsets=None, out_dtype=None, stream=None):
     """One-shot Local-Hessian calibration of a layer (see Calibrator)."""
     if W.dim() == 2:
         W = W.unsqueeze(0)
-    cal = Calibrator(W.shape[0], W.shape[1], W.shape[2], X.shape[0], offsets is not None, out_dtype,
-                     device=W.device)
-    codes, amax, Wq = cal.run(W, X, offsets, stream)
+    with _on(stream):
+        cal = Calibrator(W.shape[0], W.shape[1], W.shape[2], X.shape[0], offsets is not None, out_dtype,
+                         device=W.device)
+        codes, amax, Wq = cal.run(W, X, offsets)
     return dict(codes=codes, best_amax=amax, Wq=Wq, H=cal.H, global_amax=cal.amax)
 
 

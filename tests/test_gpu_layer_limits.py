@@ -210,3 +210,19 @@ def test_the_default_streams_handle_is_the_default_stream(cuda_ok, handle):
     y2 = q2.forward_routed(x, lh.Routing(9, 2, 3).route(i, stream=handle), stream=handle)
     torch.cuda.synchronize()
     assert torch.equal(y2, y) and all(torch.equal(got[key], want[key]) for key in want)
+
+
+def test_calibration_on_a_stream_does_all_of_it_there(cuda_ok):
+    # the current stream is busy for a while: what calibration needs set to zero must not wait for it
+    lh = _lh()
+    W, X = torch.randn(16, 64, device="cuda"), torch.randn(400, 64, device="cuda").bfloat16()
+    want = lh.calibrate(W, X)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[key]) for key, v in lh.calibrate(W, X, stream=0).items())  # the default stream
+    for stream in (s, s.cuda_stream):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        got = lh.calibrate(W, X, stream=stream)
+        s.synchronize()
+        host = {key: got[key].cpu() for key in got}  # behind the sleep
+        assert all(torch.equal(host[key], want[key].cpu()) for key in want)
