@@ -226,3 +226,61 @@ def test_calibration_on_a_stream_does_all_of_it_there(cuda_ok):
         s.synchronize()
         host = {key: got[key].cpu() for key in got}  # behind the sleep
         assert all(torch.equal(host[key], want[key].cpu()) for key in want)
+
+
+def far_rows(rng, n, k, e):
+    """(ids with masked slots, order, pos) of n tokens on the device."""
+    ids = rng.integers(0, e, (n, k)).astype(np.int32)
+    ids[rng.random((n, k)) < 0.2] = -1
+    ids[::7] = -1
+    _, order, pos = ref.route(ids, e)
+    return torch.from_numpy(order).cuda(), torch.from_numpy(pos).cuda()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("n,k,c", [(5000, 5, 521), (5000, 3, 1536), (40001, 2, 72), (2500, 9, 1030)])
+def test_rows_of_many_rounds(cuda_ok, n, k, c, t):
+    # more vectors, rows and tokens than the grids take at once, every one of them looked at
+    lh = _lh()
+    rng = np.random.default_rng(n + k)
+    dt, e = layer.DT[t], 64
+    order, pos = far_rows(rng, n, k, e)
+    R = n * k
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(c)
+
+    def rows(m, fill):
+        b = torch.full((m, layer.pitch(c, t)), fill, dtype=dt, device="cuda")
+        b[:, :c] = torch.randn(m, c, generator=gen, device="cuda")
+        return b
+
+    x, ys, dy = rows(n, -7.0), rows(R, -7.0), rows(n, -7.0)
+    w = torch.randn(n, k, generator=gen, device="cuda")
+    named = order >= 0
+    xs = torch.full_like(ys, 3.0)
+    lh.lh_gather_tokens(x, x, n, c, x.stride(0), order, k, R, xs, xs.stride(0))
+    want = torch.full_like(xs, 3.0)
+    want[named, :c] = x[order[named].long() // k, :c]
+    assert torch.equal(xs, want)
+
+    ys[~named] = float("nan")  # read by nothing
+    y = torch.full_like(x, 5.0)
+    lh.lh_combine_tokens(ys, ys, R, c, ys.stride(0), pos, w, n, k, y, y.stride(0))
+    there = (pos >= 0).view(n, k)
+    taken = torch.where(there[..., None], ys[pos.clamp(min=0).long(), :c].view(n, k, c).double(), 0.0)
+    terms = w.double()[..., None] * taken
+    sums, mag = terms.sum(1), terms.abs().sum(1)
+    tol = k * 2.0 ** -24 * mag  # k fused multiply-adds, each rounded once
+    tol = tol + (sums.abs() + tol) * layer.HALF[t]
+    assert ((y[:, :c].double() - sums).abs() <= tol).all() and (y[:, c:] == 5.0).all()
+
+    dys, dw = torch.full_like(ys, 9.0), torch.full_like(w, 9.0)
+    lh.lh_combine_tokens_grad(dy, dy, n, k, c, dy.stride(0), ys, ys.stride(0), R, pos, w, dys, dys.stride(0), dw)
+    d = dy[:, :c].double()
+    want = torch.full((R, c), 9.0, dtype=torch.float64, device="cuda")
+    want[pos[there.view(-1)].long()] = (w.double()[..., None] * d[:, None])[there]
+    # one product rounded to FP32, then to the type
+    assert ((dys[:, :c].double() - want).abs() <= want.abs() * (2.0 ** -24 + layer.HALF[t] * (1 + 2.0 ** -24))).all()
+    assert (dys[:, c:] == 9.0).all()
+    dots, size = (d[:, None] * taken).sum(2), (d[:, None] * taken).abs().sum(2)
+    assert ((dw.double() - dots).abs() <= (c + 5) * 2.0 ** -24 * size).all()  # c products and sums in FP32
