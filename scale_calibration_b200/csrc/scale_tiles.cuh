@@ -23,9 +23,5 @@ constexpr int kTileBytes = 512;
 
 __host__ __device__ __forceinline__ int64_t scale_steps(int64_t c_in) { return (c_in + 63) / 64; }
 __host__ __device__ __forceinline__ int64_t group_tile(int64_t first_row, int64_t g) { return first_row / kTileRows + g; }
-// Offset of block 4 k + j of row r of a tile, within the tile's row of steps.
-__host__ __device__ __forceinline__ int64_t scale_offset(int64_t tile, int r, int64_t k, int64_t steps) {
-    return (tile * steps + k) * kTileBytes + (r & 31) * 16 + (r >> 5) * 4;
-}
 
 }  // namespace lh
