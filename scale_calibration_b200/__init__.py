@@ -62,6 +62,10 @@ class Calibrator:
         n_mats, c_out, c_in = self.n_mats, self.c_out, self.c_in
         if X.dtype != torch.bfloat16:
             raise ValueError(f"X must be bf16, not {X.dtype}")
+        if X.dim() != 2 or X.shape[1] != c_in:
+            raise ValueError(f"X must be [n_tok, {c_in}], not {tuple(X.shape)}")
+        if W.dim() not in (2, 3) or tuple(W.shape) != (n_mats, c_out, c_in)[3 - W.dim():] or W.numel() != n_mats * c_out * c_in:
+            raise ValueError(f"W must be [{n_mats}, {c_out}, {c_in}], not {tuple(W.shape)}")
         if self.grouped:
             _typed("offsets", offsets, torch.int64, self.n_groups + 1)
         with _on(stream):

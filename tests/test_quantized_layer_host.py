@@ -100,3 +100,16 @@ def test_tensors_have_to_be_on_the_streams_device(monkeypatch):
                  lambda: lh.calibrate_routed(gpu0(torch.zeros(3, 8, 64)), gpu0(torch.zeros(10, 64).bfloat16()), ids)):
         with pytest.raises(ValueError, match="is on cuda:0, the current device is cuda:1"):
             call()
+
+
+def test_calibration_refuses_other_shapes():
+    # rows and matrices past the tensors' ends would be read
+    lh = _lh()
+    cal = lh.Calibrator(2, 8, 64, 5, True, device="cpu")
+    off, x, w = torch.zeros(3, dtype=torch.int64), torch.zeros(5, 64).bfloat16(), torch.zeros(2, 8, 64)
+    for bad in (torch.zeros(5, 80)[:, :48], torch.zeros(5, 80), torch.zeros(5, 1, 64)):
+        with pytest.raises(ValueError, match="X must be"):
+            cal.run(w, bad.bfloat16(), off)
+    for bad in (w[:1], w[0], torch.zeros(2, 8, 48), torch.zeros(2, 4, 64), torch.zeros(2, 2, 8, 64)):
+        with pytest.raises(ValueError, match="W must be"):
+            cal.run(bad, x, off)
