@@ -57,6 +57,29 @@ def test_the_most_rows_of_tokens(big):
         assert torch.equal(w[:b - a], rc.view(-1)[rows[a:b].long()].to(torch.int32))
 
 
+def test_the_most_rows_of_a_product(big):
+    # 2^31 - 513 rows of 32 values by 8 channels: every row equals that of the same token in a small call
+    lh = _lh()
+    n, m, c, n_src = (1 << 31) - 513, 8, 32, 37
+    rng = np.random.default_rng(1)
+    w, _, _ = layer.bank(rng, 1, m, c)
+    x = torch.from_numpy(rng.standard_normal((n_src, c)).astype(np.float32)).cuda()
+    small = torch.zeros(n_src, m, dtype=torch.bfloat16, device="cuda")
+    layer.linear(x, n_src, c, w, m, small)
+    rows = torch.empty(n, dtype=torch.int32, device="cuda")
+    for a in range(0, n, PIECE):
+        b = min(a + PIECE, n)
+        rows[a:b] = (torch.arange(a, b, device="cuda") % n_src).to(torch.int32)
+    y = torch.zeros(n, m, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(lh.lh_nvfp4_linear_workspace_bytes(n, c, 1), dtype=torch.uint8, device="cuda")
+    layer.linear(x, n_src, c, w, m, y, rows=rows, n_rows=n, ws=ws)
+    assert lh.lh_nvfp4_status() == 0
+    assert float(small.float().abs().sum()) > 0
+    for a in range(0, n, PIECE):
+        b = min(a + PIECE, n)
+        assert torch.equal(y[a:b], small[rows[a:b].long()])
+
+
 def test_the_most_ids(big):
     # 2^31 - 513 ids, every third of them without an expert
     lh = _lh()
