@@ -442,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_split_kernel(const __grid
             }
         }
     } else if (warp == 1) {
+        // the bounded waits below begin when the tokens are there, not while they are quantised
+        if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
         bool ok = true;
         const uint64_t desc_a = desc_k_sw128(ring), desc_b = desc_k_sw128(ring + S::kA);
         const uint64_t desc_sa = desc_scales(ring + S::kA + S::kB), desc_sb = desc_scales(ring + S::kA + S::kB + S::kSa);
@@ -714,6 +716,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1) {
         if (rank == 0) {
+            // the bounded waits below begin when the tokens are there, not while they are quantised
+            if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
             int stage = 0;
             uint32_t phase = 0, aphase = 0, set = 0;
             bool ok = true;
