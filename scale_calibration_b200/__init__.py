@@ -142,9 +142,11 @@ def _rows(t, what):
 
 def _matrices(W):
     """W [n_mats, c_out, c_in] (or one matrix) as rows at one distance, matrix after matrix: copied if it does not lie so."""
-    if W.stride(-1) == 1 and (W.dim() == 2 or W.shape[0] == 1 or W.stride(0) == W.stride(1) * W.shape[1]):
+    import torch
+    if W.stride(-1) == 1 and W.stride(-2) >= W.shape[-1] and (W.dim() == 2 or W.shape[0] == 1 or
+                                                              W.stride(0) == W.stride(1) * W.shape[1]):
         return W
-    return W.contiguous()
+    return W.clone(memory_format=torch.contiguous_format)  # contiguous() would keep any stride of a dimension of one
 
 
 class Routing:

@@ -307,3 +307,17 @@ def test_rows_of_many_rounds(cuda_ok, n, k, c, t):
     assert (dys[:, c:] == 9.0).all()
     dots, size = (d[:, None] * taken).sum(2), (d[:, None] * taken).abs().sum(2)
     assert ((dw.double() - dots).abs() <= (c + 5) * 2.0 ** -24 * size).all()  # c products and sums in FP32
+
+
+def test_matrices_of_one_row(cuda_ok):
+    # their row's stride is arbitrary, and a copy's was taken for the way from matrix to matrix
+    lh = _lh()
+    W = torch.randn(1, 3, 64, device="cuda").transpose(0, 1)
+    X = torch.randn(40, 64, device="cuda").bfloat16()
+    ids = (torch.arange(80, device="cuda").view(40, 2) % 3).to(torch.int32)
+    same = torch.empty(3, 1, 64, device="cuda").copy_(W)
+    assert W.stride(1) == 192 and same.stride(1) == 64
+    want, got = lh.calibrate_routed(same, X, ids), lh.calibrate_routed(W, X, ids)
+    assert all(torch.equal(got[key], want[key]) for key in want)
+    a, b = (lh.QuantizedLayer(w, want["global_amax"], want["codes"]) for w in (same, W))
+    assert torch.equal(a.packed, b.packed) and torch.equal(a.block_scales, b.block_scales)

@@ -113,3 +113,17 @@ def test_calibration_refuses_other_shapes():
     for bad in (w[:1], w[0], torch.zeros(2, 8, 48), torch.zeros(2, 4, 64), torch.zeros(2, 2, 8, 64)):
         with pytest.raises(ValueError, match="W must be"):
             cal.run(bad, x, off)
+
+
+@pytest.mark.parametrize("w", [
+    torch.arange(192.0).view(1, 3, 64).transpose(0, 1),  # [3, 1, 64] with a stride of 192 for its one row: "contiguous"
+    torch.arange(64.0).view(64, 1).t(), torch.arange(64.0).view(1, 64, 1).transpose(1, 2), torch.arange(64.0).expand(2, 3, 64),
+    torch.arange(384.0).view(2, 3, 64), torch.arange(768.0).view(4, 3, 64)[::2], torch.arange(480.0).view(2, 3, 80)[..., :64],
+    torch.arange(384.0).view(2, 64, 3).transpose(1, 2),
+])
+def test_matrices_lie_as_the_library_reads_them(w):
+    lh = _lh()
+    m = lh._matrices(w)
+    assert torch.equal(m, w) and m.stride(-1) == 1 and m.stride(-2) >= m.shape[-1]
+    if m.dim() == 3 and m.shape[0] > 1:
+        assert m.stride(0) == m.shape[1] * m.stride(1)
